@@ -73,6 +73,7 @@ extern "C" {
 #define PA_DEV_FREE_UNDERFLOW  4   /* append needed a block and the free list was empty */
 #define PA_DEV_FREE_OVERFLOW   8   /* free pushed past num_blocks entries */
 #define PA_DEV_TIMEOUT        16   /* an internal pipeline wait ran out; output invalid */
+#define PA_DEV_BAD_SCALE      32   /* 8-bit cache: a held page's scale is no power of two of the format */
 
 /*
  * pa_kv_append_rope -- append one new token per sequence to the paged cache.
@@ -542,6 +543,87 @@ int pa_decode_set_test_fault(int stage, long long wait_limit_ns);
  * Process-wide; for tests only.  PA_ERR_ARG for another mode.
  */
 int pa_decode_set_test_plan(int mode);
+
+/*
+ * The 8-bit cache -- the four operators above over pages of e4m3 values with
+ * a scale for each page, kv head and K or V (no counterpart on the pages: the
+ * page's cache is bf16).  Half the bytes of the bf16 cache: decode attention
+ * reads 1 KiB a token and layer.
+ *
+ *   kv_cache   [num_blocks][2][block_tokens][8][64] e4m3 bytes (0 = K, 1 = V)
+ *   kv_scales  [num_blocks][2][8] fp32; a value is byte * scale
+ *
+ * block_tokens is 8, 16 or 32 (PA_ERR_ARG otherwise); block tables, free
+ * list, context lengths, errors and stream behaviour are those of the bf16
+ * calls, and pa_free / pa_free_bt serve both caches (they touch no pool).
+ * Neither array needs to be initialised.  Both must be 16-byte aligned.
+ *
+ * A scale is 2^e with the smallest e >= -117 for which the largest finite
+ * magnitude of the head's values in the page is at most 448 * 2^e (V) or
+ * 316 * 2^e (K, taken before the rotation; 316 * sqrt(2) < 448, so it holds
+ * at any position).  A value is stored as the e4m3 number nearest to value /
+ * scale (ties to even; at most half a step, 2^-4 of the value, off down to
+ * 2^-15 of the page's largest); NaN and infinities are stored as NaN and do
+ * not count for the scale.
+ */
+
+/*
+ * pa_kv_append_rope_q8 / pa_prefill_append_rope_q8 -- pa_kv_append_rope and
+ * pa_prefill_append_rope into the 8-bit cache.  k is rotated and rounded to
+ * bf16 as there, then quantised with v.  A page opened by the call takes the
+ * scale of the tokens the call puts there.  A page that holds tokens keeps
+ * the larger of its scale and the new tokens'; where it grows, the tokens
+ * held are rounded to the new scale (a change of exponent: only values that
+ * become subnormal bytes lose bits).  Slots that hold no token of the
+ * sequence stay as they are.
+ * q_or_null is read and the rotated rows are written to q_out (q_out may be
+ * q_or_null; it is ignored when q_or_null is NULL, and rows of refused chunks
+ * or sequences are not written).  Same device errors, and PA_DEV_BAD_SCALE
+ * (the scale of a page that holds tokens is not a power of two of the range:
+ * that head's K or V is not stored).
+ */
+int pa_kv_append_rope_q8(const uint16_t *k_new, const uint16_t *v_new, const uint16_t *q_or_null,
+                         uint16_t *q_out, uint8_t *kv_cache, float *kv_scales, int num_blocks,
+                         int block_tokens, int32_t *block_table, int n_layers,
+                         int max_blocks_per_seq, const int32_t *context_lens, int num_seqs,
+                         int layer, int32_t *free_list, int32_t *free_count, int32_t *err,
+                         void *stream);
+int pa_prefill_append_rope_q8(const uint16_t *k_new, const uint16_t *v_new,
+                              const uint16_t *q_or_null, uint16_t *q_out, int total_tokens,
+                              const int32_t *cu_tokens, uint8_t *kv_cache, float *kv_scales,
+                              int num_blocks, int block_tokens, int32_t *block_table, int n_layers,
+                              int max_blocks_per_seq, const int32_t *context_lens, int num_seqs,
+                              int layer, int32_t *free_list, int32_t *free_count, int32_t *err,
+                              void *stream);
+
+/*
+ * pa_decode_attention_q8 -- pa_decode_attention over the 8-bit cache: q and
+ * out stay bf16, sums and the softmax are fp32.  A sequence with context 0
+ * gets a zero output, and so does one none of whose pages is valid.
+ * num_seqs is at most 2048.  workspace: pa_decode_workspace_size_q8 bytes,
+ * zero-filled once before its first use, not shared by calls that overlap in
+ * time; it is not interchangeable with pa_decode_attention's.
+ * pa_decode_set_path and pa_decode_set_grid_limit do not apply.
+ */
+int pa_decode_attention_q8(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,
+                           const float *kv_scales, int num_blocks, int block_tokens,
+                           const int32_t *block_table, int n_layers, int max_blocks_per_seq,
+                           const int32_t *context_lens, int num_seqs, int layer, float scale,
+                           void *workspace, size_t workspace_bytes, int32_t *err, void *stream);
+size_t pa_decode_workspace_size_q8(int num_seqs, int max_blocks_per_seq, int block_tokens);
+
+/*
+ * pa_prefill_attention_q8 -- pa_prefill_attention over the 8-bit cache (the
+ * chunk's own K/V already in it: pa_prefill_append_rope_q8 before this call
+ * on the same stream).  Same limits, errors and handling of refused chunks;
+ * pa_prefill_set_test_fault acts on it too.
+ */
+int pa_prefill_attention_q8(uint16_t *out, const uint16_t *q, int total_tokens,
+                            const int32_t *cu_tokens, const uint8_t *kv_cache,
+                            const float *kv_scales, int num_blocks, int block_tokens,
+                            const int32_t *block_table, int n_layers, int max_blocks_per_seq,
+                            const int32_t *context_lens, int num_seqs, int layer, float scale,
+                            int32_t *err, void *stream);
 
 /* Human-readable name of a PA_ERR_* code. */
 const char *pa_error_string(int code);

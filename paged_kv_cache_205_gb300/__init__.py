@@ -14,6 +14,14 @@ from ._binding import (  # noqa: F401
     BatchPlan,
     batch_buffers,
     pa_batcher_ctl_bytes,
+    PA_DEV_BAD_SCALE,
+    decode_workspace_q8,
+    kv_cache_q8,
+    pa_decode_attention_q8,
+    pa_decode_workspace_size_q8,
+    pa_kv_append_rope_q8,
+    pa_prefill_append_rope_q8,
+    pa_prefill_attention_q8,
     PA_BLOCK_BYTES,
     PA_BLOCK_TOKENS,
     PA_DEV_BAD_BLOCK,

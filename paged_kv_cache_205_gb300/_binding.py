@@ -22,6 +22,7 @@ PA_DEV_CTX_RANGE = 2
 PA_DEV_FREE_UNDERFLOW = 4
 PA_DEV_FREE_OVERFLOW = 8
 PA_DEV_TIMEOUT = 16
+PA_DEV_BAD_SCALE = 32
 
 _EXPORTS = (
     "pa_kv_append_rope",
@@ -52,6 +53,11 @@ _EXPORTS = (
     "pa_batcher_run",
     "pa_batcher_commit",
     "pa_batcher_set_graphs",
+    "pa_kv_append_rope_q8",
+    "pa_prefill_append_rope_q8",
+    "pa_decode_attention_q8",
+    "pa_decode_workspace_size_q8",
+    "pa_prefill_attention_q8",
 )
 
 _lock = threading.Lock()
@@ -168,6 +174,17 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.pa_batcher_commit.restype = I
         lib.pa_batcher_set_graphs.argtypes = [P, I]
         lib.pa_batcher_set_graphs.restype = I
+        lib.pa_kv_append_rope_q8.argtypes = [P, P, P, P, P, P, I, I, P, I, I, P, I, I, P, P, P, P]
+        lib.pa_kv_append_rope_q8.restype = I
+        lib.pa_prefill_append_rope_q8.argtypes = [P, P, P, P, I, P, P, P, I, I, P, I, I, P, I, I, P,
+                                                  P, P, P]
+        lib.pa_prefill_append_rope_q8.restype = I
+        lib.pa_decode_attention_q8.argtypes = [P, P, P, P, I, I, P, I, I, P, I, I, F, P, Z, P, P]
+        lib.pa_decode_attention_q8.restype = I
+        lib.pa_decode_workspace_size_q8.argtypes = [I, I, I]
+        lib.pa_decode_workspace_size_q8.restype = Z
+        lib.pa_prefill_attention_q8.argtypes = [P, P, I, P, P, P, I, I, P, I, I, P, I, I, F, P, P]
+        lib.pa_prefill_attention_q8.restype = I
         _lib = lib
         return lib
 
@@ -405,6 +422,154 @@ def pa_decode_set_path(path: int) -> None:
     """Selects the decode-attention kernel: PA_DECODE_AUTO (default),
     PA_DECODE_SPLIT or PA_DECODE_CLUSTER (process-wide)."""
     _check("pa_decode_set_path", library().pa_decode_set_path(int(path)))
+
+
+# ----------------------------------------------------------- the 8-bit cache
+def kv_cache_q8(num_blocks: int, device=None, block_tokens: int = PA_BLOCK_TOKENS):
+    """The 8-bit cache's two tensors, zeros and ones: kv_cache
+    [num_blocks][2][block_tokens][8][64] float8_e4m3fn and kv_scales
+    [num_blocks][2][8] float32 (see include/pagedkv.h)."""
+    torch = _torch()
+    if block_tokens not in (8, 16, 32):
+        raise ValueError("pages of 8, 16 or 32 tokens")
+    pool = torch.zeros((num_blocks, 2, block_tokens, PA_NUM_KV_HEADS, PA_HEAD_DIM),
+                       dtype=torch.float8_e4m3fn, device=device or "cuda")
+    scales = torch.ones((num_blocks, 2, PA_NUM_KV_HEADS), dtype=torch.float32, device=pool.device)
+    return pool, scales
+
+
+def _q8(tensors, table, heads):
+    """Checks a call of the 8-bit cache: `tensors` {name: (tensor, dtypes,
+    shape)} with None for an extent that is free, all on the current device,
+    contiguous.  Returns {name: device pointer}."""
+    torch = _torch()
+    if table.dim() != 3:
+        raise ValueError("block_table must be [num_seqs][n_layers][max_blocks_per_seq]")
+    ptr = {}
+    for name, (t, dtypes, shape) in tensors.items():
+        if t is None and name in heads:
+            ptr[name] = None
+            continue
+        ptr[name] = _dev(t, name, dtypes)
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must live on the current CUDA device")
+        if shape is not None and (t.dim() != len(shape) or
+                                  any(w is not None and w != n for n, w in zip(t.shape, shape))):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return ptr
+
+
+def _q8_cache(kv_cache, kv_scales):
+    torch = _torch()
+    blocks = int(kv_cache.shape[0]) if kv_cache.dim() == 5 else None
+    return {"kv_cache": (kv_cache, (torch.float8_e4m3fn, torch.uint8),
+                         (None, 2, None, PA_NUM_KV_HEADS, PA_HEAD_DIM)),
+            "kv_scales": (kv_scales, (torch.float32,), (blocks, 2, PA_NUM_KV_HEADS))}
+
+
+def _q8_append(fn, k_new, v_new, q, q_out, cu_tokens, kv_cache, kv_scales, block_table,
+               context_lens, layer, free_list, free_count, err, stream):
+    n, n_layers, max_blocks = block_table.shape
+    rows = int(n) if cu_tokens is None else int(k_new.shape[0])
+    if q is not None and q_out is None:
+        q_out = q
+    kv_shape, q_shape = (rows, PA_NUM_KV_HEADS, PA_HEAD_DIM), (rows, PA_NUM_Q_HEADS, PA_HEAD_DIM)
+    i32 = _i32()
+    want = {"k_new": (k_new, _bf16(), kv_shape), "v_new": (v_new, _bf16(), kv_shape),
+            "q_or_null": (q, _bf16(), q_shape),
+            "q_out": (q_out if q is not None else None, _bf16(), q_shape),
+            **_q8_cache(kv_cache, kv_scales), "block_table": (block_table, i32, None),
+            "context_lens": (context_lens, i32, None), "free_list": (free_list, i32, None),
+            "free_count": (free_count, i32, None), "err": (err, i32, None)}
+    if cu_tokens is not None:
+        want["cu_tokens"] = (cu_tokens, i32, (n + 1,))
+    p = _q8(want, block_table, ("q_or_null", "q_out"))
+    if context_lens.numel() < n:
+        raise ValueError("context_lens must hold num_seqs entries")
+    if free_list.numel() < kv_cache.shape[0]:
+        raise ValueError("free_list must hold num_blocks entries")
+    head = (p["k_new"], p["v_new"], p["q_or_null"], p["q_out"])
+    if cu_tokens is not None:
+        head += (rows, p["cu_tokens"])
+    _check(fn, getattr(library(), fn)(
+        *head, p["kv_cache"], p["kv_scales"], int(kv_cache.shape[0]), int(kv_cache.shape[2]),
+        p["block_table"], int(n_layers), int(max_blocks), p["context_lens"], int(n), int(layer),
+        p["free_list"], p["free_count"], p["err"], _stream(stream)))
+
+
+def pa_kv_append_rope_q8(k_new, v_new, q_or_null, kv_cache, kv_scales, block_table, context_lens,
+                         layer, free_list, free_count, err, stream=None, q_out=None):
+    """pa_kv_append_rope into the 8-bit cache: kv_cache
+    [num_blocks][2][page][8][64] float8_e4m3fn (or uint8), kv_scales
+    [num_blocks][2][8] float32, pages of 8, 16 or 32 tokens.  Rotated q goes
+    to q_out (default: q_or_null itself)."""
+    _q8_append("pa_kv_append_rope_q8", k_new, v_new, q_or_null, q_out, None, kv_cache, kv_scales,
+               block_table, context_lens, layer, free_list, free_count, err, stream)
+
+
+def pa_prefill_append_rope_q8(k_new, v_new, q_or_null, cu_tokens, kv_cache, kv_scales,
+                              block_table, context_lens, layer, free_list, free_count, err,
+                              stream=None, q_out=None):
+    """pa_prefill_append_rope into the 8-bit cache; rotated q goes to q_out
+    (default: q_or_null itself)."""
+    _q8_append("pa_prefill_append_rope_q8", k_new, v_new, q_or_null, q_out, cu_tokens, kv_cache,
+               kv_scales, block_table, context_lens, layer, free_list, free_count, err, stream)
+
+
+def pa_decode_workspace_size_q8(num_seqs: int, max_blocks_per_seq: int,
+                                block_tokens: int = PA_BLOCK_TOKENS) -> int:
+    return int(library().pa_decode_workspace_size_q8(int(num_seqs), int(max_blocks_per_seq),
+                                                     int(block_tokens)))
+
+
+def decode_workspace_q8(num_seqs: int, max_blocks_per_seq: int, device=None,
+                        block_tokens: int = PA_BLOCK_TOKENS):
+    """A zero-filled uint8 CUDA tensor of pa_decode_workspace_size_q8 bytes,
+    the state pa_decode_attention_q8 expects on first use."""
+    torch = _torch()
+    n = pa_decode_workspace_size_q8(num_seqs, max_blocks_per_seq, block_tokens)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_decode_attention_q8(out, q, kv_cache, kv_scales, block_table, context_lens, layer, scale,
+                           workspace, err, stream=None, num_seqs=None):
+    """pa_decode_attention over the 8-bit cache: out/q [n][32][64] bf16;
+    workspace: decode_workspace_q8.  num_seqs defaults to block_table rows."""
+    n_rows, n_layers, max_blocks = block_table.shape
+    n = int(n_rows) if num_seqs is None else int(num_seqs)
+    if n > n_rows:
+        raise ValueError("num_seqs exceeds the block table's rows")
+    i32, rows = _i32(), (None, PA_NUM_Q_HEADS, PA_HEAD_DIM)
+    p = _q8({"out": (out, _bf16(), rows), "q": (q, _bf16(), rows),
+             **_q8_cache(kv_cache, kv_scales), "block_table": (block_table, i32, None),
+             "context_lens": (context_lens, i32, None), "workspace": (workspace, None, None),
+             "err": (err, i32, None)}, block_table, ())
+    if min(out.shape[0], q.shape[0], context_lens.numel()) < n:
+        raise ValueError("out, q and context_lens must hold num_seqs rows")
+    _check("pa_decode_attention_q8", library().pa_decode_attention_q8(
+        p["out"], p["q"], p["kv_cache"], p["kv_scales"], int(kv_cache.shape[0]),
+        int(kv_cache.shape[2]), p["block_table"], int(n_layers), int(max_blocks),
+        p["context_lens"], n, int(layer), float(scale), p["workspace"],
+        int(workspace.numel() * workspace.element_size()), p["err"], _stream(stream)))
+
+
+def pa_prefill_attention_q8(out, q, cu_tokens, kv_cache, kv_scales, block_table, context_lens,
+                            layer, scale, err, stream=None):
+    """pa_prefill_attention over the 8-bit cache: out/q [T][32][64] bf16,
+    packed as for pa_prefill_append_rope_q8."""
+    n, n_layers, max_blocks = block_table.shape
+    i32, rows = _i32(), (int(q.shape[0]), PA_NUM_Q_HEADS, PA_HEAD_DIM)
+    p = _q8({"out": (out, _bf16(), rows), "q": (q, _bf16(), rows),
+             "cu_tokens": (cu_tokens, i32, (n + 1,)), **_q8_cache(kv_cache, kv_scales),
+             "block_table": (block_table, i32, None), "context_lens": (context_lens, i32, None),
+             "err": (err, i32, None)}, block_table, ())
+    if context_lens.numel() < n:
+        raise ValueError("context_lens must hold num_seqs entries")
+    _check("pa_prefill_attention_q8", library().pa_prefill_attention_q8(
+        p["out"], p["q"], int(q.shape[0]), p["cu_tokens"], p["kv_cache"], p["kv_scales"],
+        int(kv_cache.shape[0]), int(kv_cache.shape[2]), p["block_table"], int(n_layers),
+        int(max_blocks), p["context_lens"], int(n), int(layer), float(scale), p["err"],
+        _stream(stream)))
 
 
 # -------------------------------------------------------- continuous batching
