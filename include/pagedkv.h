@@ -527,7 +527,8 @@ int pa_decode_kernel_for_lengths(const int32_t *context_lens, int num_seqs, int 
  * PA_DEV_TIMEOUT in *err and returns, and the outputs of that call are
  * undefined.  No other kernel is affected.  stage = -1 restores normal
  * operation (waits of 1 s, no copy left out).  Process-wide; for tests only.
- * Returns PA_ERR_ARG for a bad stage or limit.
+ * Returns PA_ERR_ARG for a bad stage or limit.  (pa_decode_attention_q8 has the
+ * same hook under the same setting.)
  */
 int pa_decode_set_test_fault(int stage, long long wait_limit_ns);
 

@@ -98,6 +98,8 @@ def library_path() -> str:
 def library(build_if_missing: bool = True) -> ctypes.CDLL:
     """Loads the in-tree library (building it first if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -438,63 +440,110 @@ def kv_cache_q8(num_blocks: int, device=None, block_tokens: int = PA_BLOCK_TOKEN
     return pool, scales
 
 
-def _q8(tensors, table, heads):
-    """Checks a call of the 8-bit cache: `tensors` {name: (tensor, dtypes,
-    shape)} with None for an extent that is free, all on the current device,
-    contiguous.  Returns {name: device pointer}."""
-    torch = _torch()
-    if table.dim() != 3:
+class _Types:
+    """The dtypes the 8-bit cache's calls accept, and torch's raw accessors
+    of the current device and stream (a call's host time counts: a small
+    batch's kernels take a few microseconds)."""
+
+    def __init__(self):
+        torch = _torch()
+        self.bf16, self.i32 = _bf16(), _i32()
+        self.q8, self.f32 = (torch.float8_e4m3fn, torch.uint8), (torch.float32,)
+        self.device = torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_types = None
+
+
+def _q8_types() -> _Types:
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types
+
+
+def _ptr(t, name, dtypes, dev):
+    """Device pointer of a contiguous tensor on device `dev`; raises otherwise."""
+    if t.__class__.__name__ in ("Tensor", "Parameter") and t.get_device() == dev and \
+            (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtypes)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on the current CUDA device ({dev})")
+    return t.data_ptr()
+
+
+def _shaped(t, name, dtypes, dev, shape):
+    p = _ptr(t, name, dtypes, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return p
+
+
+def _q8_cache(ty, kv_cache, kv_scales, dev):
+    """(pool pointer, scales pointer, num_blocks, block_tokens)"""
+    kv = _ptr(kv_cache, "kv_cache", ty.q8, dev)
+    shape = kv_cache.shape
+    if len(shape) != 5 or shape[1] != 2 or shape[3] != PA_NUM_KV_HEADS or shape[4] != PA_HEAD_DIM:
+        raise ValueError(f"kv_cache has shape {tuple(shape)}, expected [num_blocks][2][page][8][64]")
+    sc = _shaped(kv_scales, "kv_scales", ty.f32, dev, (shape[0], 2, PA_NUM_KV_HEADS))
+    return kv, sc, shape[0], shape[2]
+
+
+def _q8_table(block_table):
+    shape = block_table.shape
+    if len(shape) != 3:
         raise ValueError("block_table must be [num_seqs][n_layers][max_blocks_per_seq]")
-    ptr = {}
-    for name, (t, dtypes, shape) in tensors.items():
-        if t is None and name in heads:
-            ptr[name] = None
-            continue
-        ptr[name] = _dev(t, name, dtypes)
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} must live on the current CUDA device")
-        if shape is not None and (t.dim() != len(shape) or
-                                  any(w is not None and w != n for n, w in zip(t.shape, shape))):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return ptr
+    return shape
 
 
-def _q8_cache(kv_cache, kv_scales):
-    torch = _torch()
-    blocks = int(kv_cache.shape[0]) if kv_cache.dim() == 5 else None
-    return {"kv_cache": (kv_cache, (torch.float8_e4m3fn, torch.uint8),
-                         (None, 2, None, PA_NUM_KV_HEADS, PA_HEAD_DIM)),
-            "kv_scales": (kv_scales, (torch.float32,), (blocks, 2, PA_NUM_KV_HEADS))}
+def _q8_device(ty, kv_cache):
+    """The current device; a tensor elsewhere is refused by name."""
+    if not kv_cache.is_cuda:
+        raise ValueError("kv_cache must live on a CUDA device")
+    return ty.device()
+
+
+def _q8_stream(ty, stream, dev):
+    return ty.raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _q8_append(fn, k_new, v_new, q, q_out, cu_tokens, kv_cache, kv_scales, block_table,
                context_lens, layer, free_list, free_count, err, stream):
-    n, n_layers, max_blocks = block_table.shape
-    rows = int(n) if cu_tokens is None else int(k_new.shape[0])
-    if q is not None and q_out is None:
-        q_out = q
-    kv_shape, q_shape = (rows, PA_NUM_KV_HEADS, PA_HEAD_DIM), (rows, PA_NUM_Q_HEADS, PA_HEAD_DIM)
-    i32 = _i32()
-    want = {"k_new": (k_new, _bf16(), kv_shape), "v_new": (v_new, _bf16(), kv_shape),
-            "q_or_null": (q, _bf16(), q_shape),
-            "q_out": (q_out if q is not None else None, _bf16(), q_shape),
-            **_q8_cache(kv_cache, kv_scales), "block_table": (block_table, i32, None),
-            "context_lens": (context_lens, i32, None), "free_list": (free_list, i32, None),
-            "free_count": (free_count, i32, None), "err": (err, i32, None)}
-    if cu_tokens is not None:
-        want["cu_tokens"] = (cu_tokens, i32, (n + 1,))
-    p = _q8(want, block_table, ("q_or_null", "q_out"))
+    ty = _q8_types()
+    dev = _q8_device(ty, kv_cache)
+    n, n_layers, max_blocks = _q8_table(block_table)
+    bf16, i32 = ty.bf16, ty.i32
+    rows = n if cu_tokens is None else k_new.shape[0]
+    kv_shape = (rows, PA_NUM_KV_HEADS, PA_HEAD_DIM)
+    k = _shaped(k_new, "k_new", bf16, dev, kv_shape)
+    v = _shaped(v_new, "v_new", bf16, dev, kv_shape)
+    qi = qo = None
+    if q is not None:
+        q_shape = (rows, PA_NUM_Q_HEADS, PA_HEAD_DIM)
+        qi = _shaped(q, "q_or_null", bf16, dev, q_shape)
+        qo = qi if q_out is None else _shaped(q_out, "q_out", bf16, dev, q_shape)
+    kv, sc, blocks, page = _q8_cache(ty, kv_cache, kv_scales, dev)
+    table = _ptr(block_table, "block_table", i32, dev)
+    ctx = _ptr(context_lens, "context_lens", i32, dev)
+    fl = _ptr(free_list, "free_list", i32, dev)
+    fc, e = _ptr(free_count, "free_count", i32, dev), _ptr(err, "err", i32, dev)
     if context_lens.numel() < n:
         raise ValueError("context_lens must hold num_seqs entries")
-    if free_list.numel() < kv_cache.shape[0]:
+    if free_list.numel() < blocks:
         raise ValueError("free_list must hold num_blocks entries")
-    head = (p["k_new"], p["v_new"], p["q_or_null"], p["q_out"])
-    if cu_tokens is not None:
-        head += (rows, p["cu_tokens"])
-    _check(fn, getattr(library(), fn)(
-        *head, p["kv_cache"], p["kv_scales"], int(kv_cache.shape[0]), int(kv_cache.shape[2]),
-        p["block_table"], int(n_layers), int(max_blocks), p["context_lens"], int(n), int(layer),
-        p["free_list"], p["free_count"], p["err"], _stream(stream)))
+    st = _q8_stream(ty, stream, dev)
+    lib = library()
+    if cu_tokens is None:
+        rc = lib.pa_kv_append_rope_q8(k, v, qi, qo, kv, sc, blocks, page, table, n_layers,
+                                      max_blocks, ctx, n, int(layer), fl, fc, e, st)
+    else:
+        cu = _shaped(cu_tokens, "cu_tokens", i32, dev, (n + 1,))
+        rc = lib.pa_prefill_append_rope_q8(k, v, qi, qo, rows, cu, kv, sc, blocks, page, table,
+                                           n_layers, max_blocks, ctx, n, int(layer), fl, fc, e, st)
+    if rc:
+        raise PagedKVError(fn, rc)
 
 
 def pa_kv_append_rope_q8(k_new, v_new, q_or_null, kv_cache, kv_scales, block_table, context_lens,
@@ -535,41 +584,51 @@ def pa_decode_attention_q8(out, q, kv_cache, kv_scales, block_table, context_len
                            workspace, err, stream=None, num_seqs=None):
     """pa_decode_attention over the 8-bit cache: out/q [n][32][64] bf16;
     workspace: decode_workspace_q8.  num_seqs defaults to block_table rows."""
-    n_rows, n_layers, max_blocks = block_table.shape
-    n = int(n_rows) if num_seqs is None else int(num_seqs)
-    if n > n_rows:
+    ty = _q8_types()
+    rows, n_layers, max_blocks = _q8_table(block_table)
+    n = rows if num_seqs is None else int(num_seqs)
+    if n > rows:
         raise ValueError("num_seqs exceeds the block table's rows")
-    i32, rows = _i32(), (None, PA_NUM_Q_HEADS, PA_HEAD_DIM)
-    p = _q8({"out": (out, _bf16(), rows), "q": (q, _bf16(), rows),
-             **_q8_cache(kv_cache, kv_scales), "block_table": (block_table, i32, None),
-             "context_lens": (context_lens, i32, None), "workspace": (workspace, None, None),
-             "err": (err, i32, None)}, block_table, ())
-    if min(out.shape[0], q.shape[0], context_lens.numel()) < n:
-        raise ValueError("out, q and context_lens must hold num_seqs rows")
-    _check("pa_decode_attention_q8", library().pa_decode_attention_q8(
-        p["out"], p["q"], p["kv_cache"], p["kv_scales"], int(kv_cache.shape[0]),
-        int(kv_cache.shape[2]), p["block_table"], int(n_layers), int(max_blocks),
-        p["context_lens"], n, int(layer), float(scale), p["workspace"],
-        int(workspace.numel() * workspace.element_size()), p["err"], _stream(stream)))
+    dev = _q8_device(ty, kv_cache)
+    o, qi = _ptr(out, "out", ty.bf16, dev), _ptr(q, "q", ty.bf16, dev)
+    for name, s in (("out", out.shape), ("q", q.shape)):
+        if len(s) != 3 or s[0] < n or s[1] != PA_NUM_Q_HEADS or s[2] != PA_HEAD_DIM:
+            raise ValueError(f"{name} has shape {tuple(s)}, expected at least [{n}][32][64]")
+    kv, sc, blocks, page = _q8_cache(ty, kv_cache, kv_scales, dev)
+    table = _ptr(block_table, "block_table", ty.i32, dev)
+    ctx = _ptr(context_lens, "context_lens", ty.i32, dev)
+    if context_lens.numel() < n:
+        raise ValueError("context_lens must hold num_seqs entries")
+    ws, e = _ptr(workspace, "workspace", None, dev), _ptr(err, "err", ty.i32, dev)
+    rc = library().pa_decode_attention_q8(
+        o, qi, kv, sc, blocks, page, table, n_layers, max_blocks, ctx, n, int(layer), float(scale),
+        ws, workspace.numel() * workspace.element_size(), e, _q8_stream(ty, stream, dev))
+    if rc:
+        raise PagedKVError("pa_decode_attention_q8", rc)
 
 
 def pa_prefill_attention_q8(out, q, cu_tokens, kv_cache, kv_scales, block_table, context_lens,
                             layer, scale, err, stream=None):
     """pa_prefill_attention over the 8-bit cache: out/q [T][32][64] bf16,
     packed as for pa_prefill_append_rope_q8."""
-    n, n_layers, max_blocks = block_table.shape
-    i32, rows = _i32(), (int(q.shape[0]), PA_NUM_Q_HEADS, PA_HEAD_DIM)
-    p = _q8({"out": (out, _bf16(), rows), "q": (q, _bf16(), rows),
-             "cu_tokens": (cu_tokens, i32, (n + 1,)), **_q8_cache(kv_cache, kv_scales),
-             "block_table": (block_table, i32, None), "context_lens": (context_lens, i32, None),
-             "err": (err, i32, None)}, block_table, ())
+    ty = _q8_types()
+    n, n_layers, max_blocks = _q8_table(block_table)
+    dev = _q8_device(ty, kv_cache)
+    rows = q.shape[0]
+    shape = (rows, PA_NUM_Q_HEADS, PA_HEAD_DIM)
+    o = _shaped(out, "out", ty.bf16, dev, shape)
+    qi = _shaped(q, "q", ty.bf16, dev, shape)
+    cu = _shaped(cu_tokens, "cu_tokens", ty.i32, dev, (n + 1,))
+    kv, sc, blocks, page = _q8_cache(ty, kv_cache, kv_scales, dev)
+    table = _ptr(block_table, "block_table", ty.i32, dev)
+    ctx = _ptr(context_lens, "context_lens", ty.i32, dev)
     if context_lens.numel() < n:
         raise ValueError("context_lens must hold num_seqs entries")
-    _check("pa_prefill_attention_q8", library().pa_prefill_attention_q8(
-        p["out"], p["q"], int(q.shape[0]), p["cu_tokens"], p["kv_cache"], p["kv_scales"],
-        int(kv_cache.shape[0]), int(kv_cache.shape[2]), p["block_table"], int(n_layers),
-        int(max_blocks), p["context_lens"], int(n), int(layer), float(scale), p["err"],
-        _stream(stream)))
+    rc = library().pa_prefill_attention_q8(
+        o, qi, rows, cu, kv, sc, blocks, page, table, n_layers, max_blocks, ctx, n, int(layer),
+        float(scale), _ptr(err, "err", ty.i32, dev), _q8_stream(ty, stream, dev))
+    if rc:
+        raise PagedKVError("pa_prefill_attention_q8", rc)
 
 
 # -------------------------------------------------------- continuous batching

@@ -981,6 +981,11 @@ namespace pa {
 
 int decode_path_setting() { return g_decode_path; }
 
+void decode_fault(int *stage, unsigned long long *wait_ns) {
+  *stage = g_fault_stage;
+  *wait_ns = g_fault_stage >= 0 ? g_fault_wait_ns : kWaitLimitNs;
+}
+
 int decode_attention_path(uint16_t *out, const uint16_t *q, const uint16_t *kv_cache,
                           int num_blocks, int block_tokens, const int32_t *block_table,
                           int n_layers, int max_blocks_per_seq, const int32_t *context_lens,

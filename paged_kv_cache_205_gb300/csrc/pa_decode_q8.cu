@@ -4,20 +4,23 @@
 //
 // decode_q8_kernel: the 16-token tiles of all sequences are laid end to end
 // and cut into chunks; a CTA takes its own index first, then chunks from a
-// counter in the workspace.  A CTA is 8 warps, one per kv head; a warp reads
-// its head's K and V of a tile straight from global memory into the
-// registers that the MMAs take them from, several tiles ahead, so there is no
-// shared-memory ring and no barrier in the loop.  That works because the
-// sums of a dot product may be taken in any order, so the MMAs' inner and
-// output dimensions are permuted to what wide loads deliver:
-//   S = Q K^T  lane (g, c) (g = lane / 4, c = lane % 4) loads dims 16c..16c+15
-//              of tokens g and g + 8 (two 16-byte loads); k-step ks of the
-//              m16n8k16 MMAs takes dims 16c + 4 ks + {0, 1} and {2, 3} where
-//              the plain order has 2c + {0, 1} and 8 + 2c + {0, 1}.
-//   O = P V    lane (g, c) loads dims 8g..8g+7 of tokens 2c, 2c+1, 2c+8, 2c+9
-//              (four 8-byte loads); output column g of MMA nt is dim 8g + nt,
-//              so a lane ends with the 16 consecutive dims 16c..16c+15 of its
-//              q head.
+// counter in the workspace.  A producer warp streams tiles into a ring of
+// shared-memory stages, one 16 KiB TMA copy (16 tokens x 8 kv heads x K, V)
+// and one 64-byte copy of the page's scales a tile, and runs ahead over chunk
+// and sequence borders; eight consumer warps, one per kv head, follow.
+// (Tiles loaded by the consumer warps themselves, straight into the MMAs'
+// registers and two tiles ahead, reached 2.9 TB/s of the copy peak's 6.8 on 256
+// ragged sequences: each chunk's first loads waited for its page ids.)
+//
+// A consumer's inner and output dimensions are permuted to what wide
+// shared-memory loads deliver (a sum may be taken in any order):
+//   S = Q K^T  lane (g, c) (g = lane / 4, c = lane % 4) reads dims 16c..16c+15
+//              of tokens g and g + 8 (one 16-byte load each); k-step ks of
+//              the m16n8k16 MMAs takes dims 16c + 4 ks + {0, 1} and {2, 3}.
+//   O = P V    ldmatrix.trans on byte pairs: a register holds dims 2g, 2g + 1
+//              of a 16-dim group for tokens 2c, 2c + 1; one byte permute and
+//              two conversions make the B operands of two MMAs, whose columns
+//              are the group's even and odd dims.
 // e4m3 becomes f16 exactly; q is scaled by a power of two per head to f16
 // (exact for values down to 2^-29 of the head's largest).  P <= 1 enters the
 // MMA in f16: half a step is 2^-12 of a weight (2^-25 absolute below 2^-14),
@@ -26,6 +29,7 @@
 // to the running output, in the FMA that rescales it anyway.
 #include <climits>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include "pa_decode_tile.cuh"
 #include "pa_host.h"
@@ -34,15 +38,28 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = kHkv;               // one per kv head
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = kHkv;               // consumer warps, one per kv head
+constexpr int kThreads = (kWarps + 1) * 32;   // + producer warp
+constexpr int kScanThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
+constexpr int kStages = 6;
 constexpr int kMaxSeqs = 2048;             // tile prefix kept in shared memory
 constexpr int kMaxGrid = 512;
 constexpr int kChunksPerCta = 4;           // average chunks a CTA takes
 constexpr int kTile = 16;                  // tokens
-constexpr int kAhead = 2;                  // tiles in flight per warp beside the one worked on
+constexpr int kTileBytes = 2 * kTile * kQ8TokBytes;   // K and V of 8 heads: 16 KiB
 constexpr float kLog2e = 1.4426950408889634f;
+
+constexpr int kSegStart = 1;   // first tile of a (chunk, sequence) piece
+constexpr int kSegEnd = 2;     // last tile of that piece
+constexpr int kEndOfWork = 4;  // no more tiles; the stage carries no data
+
+struct StageDesc {
+  int seq;
+  int flags;
+  int slot;      // partial slot of the piece, or -1: the sequence is in one piece
+  uint32_t use;  // bit t: token t of the tile is used
+};
 
 struct Q8DecodeParams {
   __nv_bfloat16 *out;
@@ -64,12 +81,21 @@ struct Q8DecodeParams {
   int cap_tokens;
   float qscale;        // scale * log2(e)
   long long n_slots;
+  // test hook (pa_decode_set_test_fault): the stage of CTA 0 whose copies are
+  // left out (-1: none), and the limit of every wait
+  int fault_stage;
+  unsigned long long wait_ns;
 };
 
-struct Smem {
-  int prefix[kMaxSeqs + 1];   // tiles of sequences 0..s-1
+struct __align__(1024) Smem {
+  unsigned char kv[kStages][kTileBytes];   // [K|V][head][16 tokens][64], 64-byte swizzled; 8-token
+                                           // pages: two of [K|V][head][8][64]
+  float scale[kStages][2][2 * kHkv];       // [page of the tile][K|V][head]
+  int prefix[kMaxSeqs + 1];                // tiles of sequences 0..s-1
+  StageDesc desc[kStages];
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
   int warp_sum[kWarps];
-  int next;
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
@@ -90,21 +116,6 @@ __device__ __forceinline__ void mma_f16_1688(float (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(0u), "r"(b0));
 }
 
-// Loads of pool data: once used, not kept in L1.  (volatile: they stay where
-// they are written, ahead of the tile that is worked on.)
-__device__ __forceinline__ uint4 load16(const unsigned char *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 load8(const unsigned char *p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
 // Packed two-lane fp32 product.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   unsigned long long ra, rb, rd;
@@ -122,22 +133,22 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return r;
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// One tile of one kv head as loaded.
-struct TileRegs {
-  uint4 k[2];          // tokens g, g + 8: dims 16c..16c+15
-  uint2 v[4];          // tokens 2c, 2c+1, 2c+8, 2c+9: dims 8g..8g+7
-  float sk[2], sv[2];  // scales of the tile's first and second 8 tokens
-  int n_valid;         // tokens to use: 0..16
-  uint32_t use;        // 8-token pages: bit t = token t is used
-};
-
 // A warp's running softmax of one kv head: q head g (rows g < 4 are real),
-// dims 16c + nt (o[nt].x) and 16c + 8 + nt (o[nt].y).
+// dims 16 i + 4c + {0, 2} (o[2 i]) and {1, 3} (o[2 i + 1]).
 struct State {
   float2 o[8];
   float m, l;
@@ -147,10 +158,15 @@ struct State {
 #pragma unroll
     for (int t = 0; t < 8; ++t) o[t] = make_float2(0.f, 0.f);
   }
+  // dims 16 i + 4c .. + 3
+  __device__ __forceinline__ float4 dims(int i) const {
+    return make_float4(o[2 * i].x, o[2 * i + 1].x, o[2 * i].y, o[2 * i + 1].y);
+  }
 };
 
 // q head g of the group in f16, scaled by a power of two to [2^12, 2^13);
-// returns the row's score factor: qscale / that power.
+// returns the row's score factor: qscale / that power.  Lane c holds dims
+// 16c .. 16c+15 (the order of the K loads).
 __device__ __forceinline__ float load_q(const uint16_t *q_token, int head0, int g, int c,
                                         float qscale, uint32_t (&qa)[8]) {
   uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
@@ -175,36 +191,45 @@ __device__ __forceinline__ float load_q(const uint16_t *q_token, int head0, int 
   return qscale * down;
 }
 
-// Folds a tile into the state.  qa[2 ks], qa[2 ks + 1]: the A operand of k-step ks.
+// Folds a tile into the state.  k0 / k1: the head's K rows of tokens 0..7 and
+// 8..15 in shared memory, v0 / v1 its V rows.  use: tokens to use (not 0).
 template <int BT>
-__device__ __forceinline__ void attend(TileRegs &t, const uint32_t (&qa)[8], float qs, int c,
-                                       State &st) {
-  const bool part = BT == 8 ? t.use != 0xffffu : t.n_valid < kTile;
-  bool u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
-    u[i] = BT == 8 ? ((t.use >> tok) & 1u) != 0 : tok < t.n_valid;
-  }
-  if (part) {
+__device__ __forceinline__ void attend(uint32_t k0, uint32_t k1, uint32_t v0, uint32_t v1,
+                                       float2 sk, float2 sv, uint32_t use, const uint32_t (&qa)[8],
+                                       float qs, int lane, State &st) {
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t koff = g * kQ8HeadBytes + ((c ^ ((g >> 1) & 3)) << 4);
+  const uint4 ka = lds16(k0 + koff), kb = lds16(k1 + koff);
+  const int r = lane & 7;
+  const uint32_t voff = r * kQ8HeadBytes + (((lane >> 3) ^ ((r >> 1) & 3)) << 4);
+  uint32_t va[4], vb[4];
+  ldsm_x4_trans(v0 + voff, va[0], va[1], va[2], va[3]);
+  ldsm_x4_trans(v1 + voff, vb[0], vb[1], vb[2], vb[3]);
+  bool u[4] = {true, true, true, true};
+  if (use != 0xffffu) {
     // unused tokens may hold anything, NaN included: they meet P = 0
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!u[i]) t.v[i] = make_uint2(0, 0);
+    for (int i = 0; i < 4; ++i) u[i] = (use >> (2 * c + (i & 1) + 8 * (i >> 1))) & 1u;
+    const uint32_t ma = (u[0] ? 0xffffu : 0u) | (u[1] ? 0xffff0000u : 0u);
+    const uint32_t mb = (u[2] ? 0xffffu : 0u) | (u[3] ? 0xffff0000u : 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      va[i] &= ma;
+      vb[i] &= mb;
+    }
   }
   // ---- S = Q K^T for tokens 0..7 (s0) and 8..15 (s1)
   float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-  const uint32_t k0[4] = {t.k[0].x, t.k[0].y, t.k[0].z, t.k[0].w};
-  const uint32_t k1[4] = {t.k[1].x, t.k[1].y, t.k[1].z, t.k[1].w};
+  const uint32_t kw0[4] = {ka.x, ka.y, ka.z, ka.w}, kw1[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    mma_f16_16816(s0, qa[2 * ks], qa[2 * ks + 1], e4m3x2_to_f16x2(k0[ks]),
-                  e4m3x2_to_f16x2(k0[ks] >> 16));
-    mma_f16_16816(s1, qa[2 * ks], qa[2 * ks + 1], e4m3x2_to_f16x2(k1[ks]),
-                  e4m3x2_to_f16x2(k1[ks] >> 16));
+    mma_f16_16816(s0, qa[2 * ks], qa[2 * ks + 1], e4m3x2_to_f16x2(kw0[ks]),
+                  e4m3x2_to_f16x2(kw0[ks] >> 16));
+    mma_f16_16816(s1, qa[2 * ks], qa[2 * ks + 1], e4m3x2_to_f16x2(kw1[ks]),
+                  e4m3x2_to_f16x2(kw1[ks] >> 16));
   }
   // ---- online softmax of row g over tokens 2c, 2c+1, 2c+8, 2c+9
-  const float f0 = qs * t.sk[0], f1 = BT == 8 ? qs * t.sk[1] : f0;
+  const float f0 = qs * sk.x, f1 = BT == 8 ? qs * sk.y : f0;
   const float x0 = u[0] ? s0[0] * f0 : neg_inf();
   const float x1 = u[1] ? s0[1] * f0 : neg_inf();
   const float x2 = u[2] ? s1[0] * f1 : neg_inf();
@@ -220,31 +245,27 @@ __device__ __forceinline__ void attend(TileRegs &t, const uint32_t (&qa)[8], flo
   st.l = fmaf(st.l, alpha, (p0 + p1) + (p2 + p3));
   st.m = m_new;
   const uint32_t pa = f16x2(p0, p1), pc = f16x2(p2, p3);
-  // ---- O = alpha O + sV P V, 8 dims a step
+  // ---- O = alpha O + sV P V, 16 dims a step: the even ones, the odd ones
   const float2 al = make_float2(alpha, alpha);
-  const float2 sv0 = make_float2(t.sv[0], t.sv[0]), sv1 = make_float2(t.sv[1], t.sv[1]);
+  const float2 sv0 = make_float2(sv.x, sv.x), sv1 = make_float2(sv.y, sv.y);
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {   // dims 8g + 4w .. 8g + 4w + 3
-    const uint32_t a = w ? t.v[0].y : t.v[0].x, b = w ? t.v[1].y : t.v[1].x;
-    const uint32_t d = w ? t.v[2].y : t.v[2].x, e = w ? t.v[3].y : t.v[3].x;
-    const uint32_t lo[2] = {prmt(a, b, 0x5140), prmt(a, b, 0x7362)};
-    const uint32_t hi[2] = {prmt(d, e, 0x5140), prmt(d, e, 0x7362)};
+  for (int i = 0; i < 4; ++i) {
+    // bytes (t0 d0, t0 d1, t1 d0, t1 d1) to (t0 d0, t1 d0, t0 d1, t1 d1)
+    const uint32_t a = prmt(va[i], 0u, 0x3120), b = prmt(vb[i], 0u, 0x3120);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int nt = 4 * w + i;
-      const uint32_t b0 = e4m3x2_to_f16x2(lo[i >> 1] >> (16 * (i & 1)));
-      const uint32_t b1 = e4m3x2_to_f16x2(hi[i >> 1] >> (16 * (i & 1)));
-      float r[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int odd = 0; odd < 2; ++odd) {
+      const uint32_t b0 = e4m3x2_to_f16x2(a >> (16 * odd)), b1 = e4m3x2_to_f16x2(b >> (16 * odd));
+      float2 &o = st.o[2 * i + odd];
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
       if (BT == 8) {
         // the two pages' products apart: their scales differ
-        float r2[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16_1688(r, pa, b0);
-        mma_f16_1688(r2, pc, b1);
-        st.o[nt] = fma2(make_float2(r2[0], r2[1]), sv1,
-                        fma2(make_float2(r[0], r[1]), sv0, mul2(st.o[nt], al)));
+        float d2[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16_1688(d, pa, b0);
+        mma_f16_1688(d2, pc, b1);
+        o = fma2(make_float2(d2[0], d2[1]), sv1, fma2(make_float2(d[0], d[1]), sv0, mul2(o, al)));
       } else {
-        mma_f16_16816(r, pa, pc, b0, b1);
-        st.o[nt] = fma2(make_float2(r[0], r[1]), sv0, mul2(st.o[nt], al));
+        mma_f16_16816(d, pa, pc, b0, b1);
+        o = fma2(make_float2(d[0], d[1]), sv0, mul2(o, al));
       }
     }
   }
@@ -274,97 +295,28 @@ __device__ __forceinline__ int first_seq_at(const int *prefix, int n, int b) {
   return lo;
 }
 
-// The warp's tile loads.  Lane i holds the page ids of tile j0 + i of the
-// piece (two for 8-token pages) and the scales of its head there.
-struct TileIds {
-  int blk[2];
-  float sk[2], sv[2];
-};
-
-template <int BT>
-__device__ __forceinline__ TileIds load_ids(const Q8DecodeParams &p, const int32_t *row, int j,
-                                            bool have, int n_tok, int head) {
-  TileIds t;
-#pragma unroll
-  for (int i = 0; i < (BT == 8 ? 2 : 1); ++i) {
-    t.blk[i] = -1;
-    t.sk[i] = t.sv[i] = 0.f;
-    if (have && (i == 0 || n_tok > 8)) {
-      const int blk = row[BT == 32 ? j >> 1 : BT == 8 ? 2 * j + i : j];
-      if (blk >= 0 && blk < p.num_blocks) {
-        t.blk[i] = blk;
-        const float *s = p.scales + static_cast<size_t>(blk) * 2 * kHkv + head;
-        t.sk[i] = s[0];
-        t.sv[i] = s[kHkv];
-      } else {
-        report(p.err, PA_DEV_BAD_BLOCK);
-      }
-    }
-  }
-  return t;
-}
-
-// Starts the loads of tile j (lane e of the ids holds it).  A page that is
-// missing is read as page 0 and not used.
-template <int BT>
-__device__ __forceinline__ void load_tile(const Q8DecodeParams &p, const TileIds &ids, int e, int j,
-                                          int n_tok, int head, int g, int c, TileRegs &t) {
-  constexpr size_t kPage = static_cast<size_t>(BT) * 2 * kQ8TokBytes;
-  constexpr size_t kHalf = static_cast<size_t>(BT) * kQ8TokBytes;
-  const int blk0 = __shfl_sync(0xffffffffu, ids.blk[0], e);
-  t.sk[0] = __shfl_sync(0xffffffffu, ids.sk[0], e);
-  t.sv[0] = __shfl_sync(0xffffffffu, ids.sv[0], e);
-  const unsigned char *p0 = p.kv + static_cast<size_t>(max(blk0, 0)) * kPage + head * kQ8HeadBytes;
-  if (BT == 32) p0 += (j & 1) * (kTile * kQ8TokBytes);
-  const unsigned char *p1 = p0 + 8 * kQ8TokBytes;   // tokens 8..15
-  t.n_valid = blk0 >= 0 ? n_tok : 0;
-  t.use = 0;
-  if (BT == 8) {
-    const int blk1 = __shfl_sync(0xffffffffu, ids.blk[1], e);
-    t.sk[1] = __shfl_sync(0xffffffffu, ids.sk[1], e);
-    t.sv[1] = __shfl_sync(0xffffffffu, ids.sv[1], e);
-    p1 = p.kv + static_cast<size_t>(max(blk1, 0)) * kPage + head * kQ8HeadBytes;
-    t.use = ((1u << n_tok) - 1u) & ((blk0 >= 0 ? 0x00ffu : 0u) | (blk1 >= 0 ? 0xff00u : 0u));
-  } else {
-    t.sk[1] = t.sk[0];
-    t.sv[1] = t.sv[0];
-  }
-  t.k[0] = load16(p0 + g * kQ8TokBytes + 16 * c);
-  t.k[1] = load16(p1 + g * kQ8TokBytes + 16 * c);
-  const unsigned char *v0 = p0 + kHalf + 2 * c * kQ8TokBytes + 8 * g;
-  const unsigned char *v1 = p1 + kHalf + 2 * c * kQ8TokBytes + 8 * g;
-  t.v[0] = load8(v0);
-  t.v[1] = load8(v0 + kQ8TokBytes);
-  t.v[2] = load8(v1);
-  t.v[3] = load8(v1 + kQ8TokBytes);
-}
-
-template <int BT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q8_kernel(Q8DecodeParams p) {
-  __shared__ Smem sm;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const int G = gridDim.x;
-  pdl_launch_dependents();   // the merge kernel may take its place in the queue
-  pdl_wait_primary();        // everything read below may come from the previous kernel
-
-  // ---- tile prefix over the sequences
+// Tile prefix over the sequences into sm.prefix; returns the total.  Every
+// thread of the CTA calls it.
+__device__ __forceinline__ int tile_prefix(const Q8DecodeParams &p, Smem &sm, int tid, int warp,
+                                           int lane) {
   int carry = 0;
-  for (int base = 0; base < p.num_seqs; base += kThreads) {
+  for (int base = 0; base < p.num_seqs; base += kScanThreads) {
     const int i = base + tid;
     int nb = 0;
-    if (i < p.num_seqs) {
+    if (tid < kScanThreads && i < p.num_seqs) {
       const int t = p.context_lens[i];
       if (blockIdx.x == 0 && (t < 0 || t > p.cap_tokens)) report(p.err, PA_DEV_CTX_RANGE);
       nb = (clamped_ctx(p, i) + kTile - 1) / kTile;
     }
     int incl = nb;
+    if (tid < kScanThreads) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) sm.warp_sum[warp] = incl;
     }
-    if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
     int before = 0, sum = 0;
 #pragma unroll
@@ -373,98 +325,229 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q8_kernel(Q8Decod
       if (w < warp) before += v;
       sum += v;
     }
-    if (i < p.num_seqs) sm.prefix[i + 1] = carry + before + incl;
+    if (tid < kScanThreads && i < p.num_seqs) sm.prefix[i + 1] = carry + before + incl;
     carry += sum;
     __syncthreads();
   }
   if (tid == 0) sm.prefix[0] = 0;
   __syncthreads();
-  const int total = carry;
+  return carry;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap kv_map, Q8DecodeParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                       ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = gridDim.x;
+  if (tid == 0) {
+    prefetch_tensormap(&kv_map);
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(&sm.full[st], 1);
+      mbar_init(&sm.empty[st], kWarps);
+    }
+    fence_mbar_init();
+  }
+  pdl_wait_primary();        // everything read below may come from the previous kernel
+  pdl_launch_dependents();   // the merge kernel may take its place in the queue
+  const int total = tile_prefix(p, sm, tid, warp, lane);
   const int C = chunk_tiles(total, G);
   const int n_chunks = max(1, (total + C - 1) / C);
 
-  int k = blockIdx.x;
-  while (k < n_chunks) {
-    if (tid == 0) sm.next = G + atomicAdd(p.chunk_counter, 1);
-    const int b0 = k * C, b1 = min(total, b0 + C);
-    const bool last_chunk = k == n_chunks - 1;
-    for (int s = first_seq_at(sm.prefix, p.num_seqs, b0); s < p.num_seqs; ++s) {
-      const int B = sm.prefix[s];
-      if (B >= b1 && !last_chunk) break;
-      const int nb = sm.prefix[s + 1] - B;
-      if (nb == 0) {
-        // empty context: the chunk holding its start owns it; output zero
-        uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(s) * kHq * kD);
-        for (int e = tid; e < kHq * kD * 2 / 16; e += kThreads) o[e] = make_uint4(0, 0, 0, 0);
-        if (tid == 0) p.meta[s] = make_int2(0, 0);
-        continue;
-      }
-      if (B >= b1) break;   // last chunk: only empty sequences may follow
-      const int tail = clamped_ctx(p, s) - (nb - 1) * kTile;
-      const int jb = max(b0, B) - B, je = min(b1, B + nb) - B;
-      const int k_first = B / C;
-      const int n_parts = (B + nb - 1) / C - k_first + 1;
-      const int slot = k + s;
-      if (k == k_first && tid == 0) p.meta[s] = make_int2(k_first + s, n_parts);
-      const int32_t *row =
-          p.block_table + (static_cast<size_t>(s) * p.n_layers + p.layer) * p.max_blocks;
-      uint32_t qa[8];
-      State st;
-      st.reset();
-      const float qs = load_q(p.q + static_cast<size_t>(s) * kHq * kD, warp * kGqa, g, c, p.qscale, qa);
-      for (int j0 = jb; j0 < je; j0 += 32) {
-        const int cnt = min(32, je - j0);
-        auto tok = [&](int j) { return j == nb - 1 ? tail : kTile; };
-        const TileIds ids = load_ids<BT>(p, row, j0 + lane, lane < cnt, tok(j0 + lane), warp);
-        TileRegs t[kAhead + 1];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (i < cnt) load_tile<BT>(p, ids, i, j0 + i, tok(j0 + i), warp, g, c, t[i]);
-        for (int e0 = 0; e0 < cnt; e0 += kAhead + 1) {
-#pragma unroll
-          for (int i = 0; i <= kAhead; ++i) {
-            const int e = e0 + i;
-            if (e < cnt) {
-              const int f = e + kAhead;
-              if (f < cnt)
-                load_tile<BT>(p, ids, f, j0 + f, tok(j0 + f), warp, g, c, t[(i + kAhead) % (kAhead + 1)]);
-              attend<BT>(t[i], qa, qs, c, st);
+  if (warp == kWarps) {
+    // ===================================================== producer warp ==
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    uint32_t issued = 0, issued_parity = 0;   // per stage: used / parity of its last phase
+    int published = 0;                        // stages published so far
+    int k = blockIdx.x;
+    while (k < n_chunks && ok) {
+      int next = 0;
+      if (lane == 0) next = G + atomicAdd(p.chunk_counter, 1);
+      const int b0 = k * C, b1 = min(total, b0 + C);
+      const bool last_chunk = k == n_chunks - 1;
+      for (int s = first_seq_at(sm.prefix, p.num_seqs, b0); s < p.num_seqs && ok; ++s) {
+        const int B = sm.prefix[s];
+        if (B >= b1 && !last_chunk) break;
+        const int nb = sm.prefix[s + 1] - B;
+        if (nb == 0) {
+          // empty context: the chunk holding its start owns it; output zero
+          uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(s) * kHq * kD);
+          for (int e = lane; e < kHq * kD * 2 / 16; e += 32) o[e] = make_uint4(0, 0, 0, 0);
+          if (lane == 0) p.meta[s] = make_int2(0, 0);
+          continue;
+        }
+        if (B >= b1) break;   // last chunk: only empty sequences may follow
+        const int tail = clamped_ctx(p, s) - (nb - 1) * kTile;
+        const int jb = max(b0, B) - B, je = min(b1, B + nb) - B;
+        const int k_first = B / C;
+        const int n_parts = (B + nb - 1) / C - k_first + 1;
+        if (k == k_first && lane == 0) p.meta[s] = make_int2(k_first + s, n_parts);
+        const int32_t *row =
+            p.block_table + (static_cast<size_t>(s) * p.n_layers + p.layer) * p.max_blocks;
+        for (int j0 = jb; j0 < je && ok; j0 += 32) {
+          const int cnt = min(32, je - j0);
+          // lane i: the page of tile j0 + i (two pages for 8-token pages; the
+          // second exists when the tile has more than 8 tokens)
+          int my_blk = -1, my_blk2 = -1;
+          const int mj = j0 + lane;
+          if (lane < cnt) {
+            my_blk = row[BT == 32 ? mj >> 1 : BT == 8 ? 2 * mj : mj];
+            if (BT == 8 && (mj < nb - 1 || tail > 8)) my_blk2 = row[2 * mj + 1];
+          }
+          for (int e = 0; e < cnt; ++e) {
+            const int blk = __shfl_sync(0xffffffffu, my_blk, e);
+            const int blk2 = BT == 8 ? __shfl_sync(0xffffffffu, my_blk2, e) : -1;
+            const int j = j0 + e;
+            int good = 1;
+            if (lane == 0) good = mbar_wait(&sm.empty[stage], phase ^ 1, p.wait_ns) ? 1 : 0;
+            good = __shfl_sync(0xffffffffu, good, 0);
+            if (!good) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              const int n_tok = j == nb - 1 ? tail : kTile;
+              const bool valid = blk >= 0 && blk < p.num_blocks;
+              const bool has2 = BT == 8 && n_tok > 8;
+              const bool valid2 = has2 && blk2 >= 0 && blk2 < p.num_blocks;
+              if (!valid || (has2 && !valid2)) report(p.err, PA_DEV_BAD_BLOCK);
+              StageDesc d;
+              d.seq = s;
+              d.flags = (j == jb ? kSegStart : 0) | (j == je - 1 ? kSegEnd : 0);
+              d.slot = n_parts > 1 ? k + s : -1;
+              d.use = ((1u << n_tok) - 1u) & (BT == 8 ? (valid ? 0x00ffu : 0u) | (valid2 ? 0xff00u : 0u)
+                                                      : (valid ? 0xffffu : 0u));
+              sm.desc[stage] = d;
+              constexpr int kPageCopy = BT == 8 ? kTileBytes / 2 : kTileBytes;
+              const int copies = (valid ? 1 : 0) + (valid2 ? 1 : 0);
+              mbar_arrive_expect_tx(&sm.full[stage], copies * (kPageCopy + 2 * kHkv * 4));
+              // test hook: this stage's copies are left out, so its barrier
+              // never completes and every wait on it runs out
+              const bool fault = p.fault_stage == published && blockIdx.x == 0;
+              if (valid && !fault) {
+                tma_load_5d(sm.kv[stage], &kv_map, 0, BT == 32 ? (j & 1) * kTile : 0, 0, 0, blk,
+                            &sm.full[stage]);
+                bulk_g2s(sm.scale[stage][0], p.scales + static_cast<size_t>(blk) * 2 * kHkv,
+                         2 * kHkv * 4, &sm.full[stage]);
+              }
+              if (valid2 && !fault) {
+                tma_load_5d(sm.kv[stage] + kPageCopy, &kv_map, 0, 0, 0, 0, blk2, &sm.full[stage]);
+                bulk_g2s(sm.scale[stage][1], p.scales + static_cast<size_t>(blk2) * 2 * kHkv,
+                         2 * kHkv * 4, &sm.full[stage]);
+              }
+              issued |= 1u << stage;
+              issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+            }
+            __syncwarp();
+            ++published;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1;
             }
           }
         }
       }
-      // ---- finish this piece of sequence s
-      float lt = st.l;
-      lt += __shfl_xor_sync(0xffffffffu, lt, 1);
-      lt += __shfl_xor_sync(0xffffffffu, lt, 2);
-      if (g < kGqa) {
-        const int h = warp * kGqa + g;
-        if (n_parts == 1) {
-          const float inv = lt == 0.f ? 0.f : 1.f / lt;   // 0: no page of the context is valid
-          uint32_t w[8];
+      k = __shfl_sync(0xffffffffu, next, 0);
+      if (k < G) k = n_chunks;   // a counter that was never zeroed
+    }
+    if (lane == 0) {
+      if (ok && mbar_wait(&sm.empty[stage], phase ^ 1, p.wait_ns)) {
+        sm.desc[stage].flags = kEndOfWork;
+        mbar_arrive(&sm.full[stage]);
+        // this arrive is now the stage's last phase; the copy before it on
+        // the same stage has landed, or the consumers could not have freed it
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+      } else {
+        report(p.err, PA_DEV_TIMEOUT);
+      }
+      // no copy may still be landing in shared memory when the CTA exits
+      for (int st = 0; st < kStages; ++st)
+        if ((issued >> st) & 1u)
+          if (!mbar_wait(&sm.full[st], (issued_parity >> st) & 1u, p.wait_ns))
+            report(p.err, PA_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    // ===================================================== consumer warps ==
+    const int g = lane >> 2, c = lane & 3;
+    constexpr int kRows = BT == 8 ? 8 : kTile;                  // token rows of a head in a stage
+    constexpr uint32_t kHeadTile = kRows * kQ8HeadBytes;        // one head's K (or V) there
+    constexpr uint32_t kHalf = kHkv * kHeadTile;                // V behind K
+    constexpr uint32_t kSecond = BT == 8 ? kTileBytes / 2 : 8 * kQ8HeadBytes;   // tokens 8..15
+    uint32_t qa[8];
+    float qs = 0.f;
+    State st;
+    st.reset();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[i] = float2_to_bf16x2(st.o[2 * i].x * inv, st.o[2 * i + 1].x * inv);
-            w[4 + i] = float2_to_bf16x2(st.o[2 * i].y * inv, st.o[2 * i + 1].y * inv);
+    for (int i = 0; i < 8; ++i) qa[i] = 0u;
+    int stage = 0;
+    uint32_t phase = 0;
+    while (true) {
+      if (!mbar_wait(&sm.full[stage], phase, p.wait_ns)) {
+        report(p.err, PA_DEV_TIMEOUT);
+        break;
+      }
+      const StageDesc d = sm.desc[stage];
+      if (d.flags & kEndOfWork) break;
+      if (d.flags & kSegStart) {
+        qs = load_q(p.q + static_cast<size_t>(d.seq) * kHq * kD, warp * kGqa, g, c, p.qscale, qa);
+        st.reset();
+      }
+      if (d.use) {
+        const uint32_t k0 = smem_u32(sm.kv[stage]) + warp * kHeadTile;
+        const float(&sc)[2][2 * kHkv] = sm.scale[stage];
+        float2 sk, sv;
+        sk.x = sc[0][warp];
+        sv.x = sc[0][kHkv + warp];
+        sk.y = sv.y = 0.f;
+        if (BT == 8) {
+          // a page that was not loaded left what the stage held before
+          if (!(d.use & 0x00ffu)) sk.x = sv.x = 0.f;
+          if (d.use & 0xff00u) {
+            sk.y = sc[1][warp];
+            sv.y = sc[1][kHkv + warp];
           }
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(s) * kHq + h) * kD + 16 * c);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-          float4 *dst = reinterpret_cast<float4 *>(p.acc + (static_cast<size_t>(slot) * kHq + h) * kD + 16 * c);
+        }
+        attend<BT>(k0, k0 + kSecond, k0 + kHalf, k0 + kHalf + kSecond, sk, sv, d.use, qa, qs, lane,
+                   st);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+      if (d.flags & kSegEnd) {
+        // ---- finish this piece of sequence d.seq
+        float lt = st.l;
+        lt += __shfl_xor_sync(0xffffffffu, lt, 1);
+        lt += __shfl_xor_sync(0xffffffffu, lt, 2);
+        if (g < kGqa) {
+          const int h = warp * kGqa + g;
+          if (d.slot < 0) {
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;   // 0: no page of the context is valid
+            uint2 *dst = reinterpret_cast<uint2 *>(p.out + (static_cast<size_t>(d.seq) * kHq + h) * kD + 4 * c);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            dst[i] = make_float4(st.o[4 * i].x, st.o[4 * i + 1].x, st.o[4 * i + 2].x, st.o[4 * i + 3].x);
-            dst[2 + i] = make_float4(st.o[4 * i].y, st.o[4 * i + 1].y, st.o[4 * i + 2].y, st.o[4 * i + 3].y);
+            for (int i = 0; i < 4; ++i) {
+              const float4 o = st.dims(i);
+              dst[4 * i] = make_uint2(float2_to_bf16x2(o.x * inv, o.y * inv),
+                                      float2_to_bf16x2(o.z * inv, o.w * inv));
+            }
+          } else {
+            const size_t at = static_cast<size_t>(d.slot) * kHq + h;
+            float4 *dst = reinterpret_cast<float4 *>(p.acc + at * kD + 4 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[4 * i] = st.dims(i);
+            if (c == 0) p.ml[at] = make_float2(st.m, lt);
           }
-          if (c == 0) p.ml[static_cast<size_t>(slot) * kHq + h] = make_float2(st.m, lt);
         }
       }
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
-    __syncthreads();
-    k = sm.next;
-    if (k < G) k = n_chunks;   // a counter that was never zeroed
-    __syncthreads();
   }
 }
 
@@ -551,6 +634,34 @@ long long slots_for(int num_seqs, int grid) {
   return static_cast<long long>(kChunksPerCta) * grid + 2 + num_seqs;
 }
 
+// Tensor map over the pool: dims (d 64, token bt, kv head 8, K|V 2, block),
+// the token dimension before the head dimension although its stride is the
+// larger one, so that a copy writes each head's token rows together; box
+// (64, 8 or 16, 8, 2, 1), 64-byte swizzle.
+int make_q8_tile_map(CUtensorMap *map, const void *kv_cache, int num_blocks, int bt) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &qr) != cudaSuccess ||
+        qr != cudaDriverEntryPointSuccess)
+      return PA_ERR_CUDA;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }
+  const cuuint64_t half = static_cast<cuuint64_t>(bt) * kQ8TokBytes;
+  const cuuint64_t dims[5] = {kD, static_cast<cuuint64_t>(bt), kHkv, 2,
+                              static_cast<cuuint64_t>(num_blocks)};
+  const cuuint64_t strides[4] = {kQ8TokBytes, kQ8HeadBytes, half, 2 * half};
+  const cuuint32_t box[5] = {kD, bt == 8 ? 8u : 16u, kHkv, 2, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(kv_cache), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
 WsLayout ws_layout(int num_seqs, long long slots) {
   WsLayout w;
   w.meta_off = 256;   // the chunk counter lies before it
@@ -593,12 +704,19 @@ int decode_q8_impl(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,
       !aligned16(workspace))
     return PA_ERR_ALIGN;
   DeviceInfo di;
-  const int rc = current_device(&di);
+  int rc = current_device(&di);
   if (rc != PA_OK) return rc;
   const int G = grid_for(di, num_seqs, tiles);
   const long long slots = slots_for(num_seqs, G);
   const WsLayout w = ws_layout(num_seqs, slots);
   if (w.total > workspace_bytes) return PA_ERR_WORKSPACE;
+  const size_t smem = sizeof(Smem) + 1024;   // + room to align the base to 1 KiB
+  if (cudaFuncSetAttribute(decode_q8_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  alignas(64) CUtensorMap map;
+  rc = make_q8_tile_map(&map, kv_cache, num_blocks, BT);
+  if (rc != PA_OK) return rc;
 
   Q8DecodeParams prm;
   unsigned char *ws = static_cast<unsigned char *>(workspace);
@@ -621,8 +739,9 @@ int decode_q8_impl(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,
   prm.cap_tokens = max_blocks_per_seq * BT;
   prm.qscale = scale * kLog2e;
   prm.n_slots = slots;
+  decode_fault(&prm.fault_stage, &prm.wait_ns);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (launch_pdl(decode_q8_kernel<BT>, dim3(G), dim3(kThreads), 0, st, prm) != cudaSuccess)
+  if (launch_pdl(decode_q8_kernel<BT>, dim3(G), dim3(kThreads), smem, st, map, prm) != cudaSuccess)
     return PA_ERR_CUDA;
   const cudaError_t e =
       num_seqs >= 8

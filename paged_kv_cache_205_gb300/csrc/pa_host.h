@@ -67,6 +67,10 @@ int launch_decode_pair(const CUtensorMap &map, uint16_t *out, const uint16_t *q,
                        int max_blocks_per_seq, const int32_t *context_lens, int num_seqs,
                        int layer, float scale, int32_t *err, int cluster, cudaStream_t stream);
 
+// The split-context kernels' test hook (pa_decode_set_test_fault,
+// pa_decode.cu): the stage left out (-1: none) and the limit of every wait.
+void decode_fault(int *stage, unsigned long long *wait_ns);
+
 // The prefill kernels' test hook (pa_prefill_set_test_fault, pa_prefill.cu):
 // the chunk left out (-1: none) and the limit of every wait.
 void prefill_fault(int *chunk, unsigned long long *wait_ns);

@@ -225,6 +225,27 @@ def test_decode_graph_stream_and_repeat():
     assert int(err.item()) == 0
 
 
+def test_decode_wait_that_runs_out():
+    """A tile announced but never copied (the library's test hook): the call
+    reports the time-out, and the next one on the workspace is right.  (Stage
+    0: the only tile that CTA 0 takes whatever the others do.)"""
+    pk = _pk()
+    lens = [900, 33, 700]
+    rng, pool, scales, table, _ = _cache(31, lens, 16)
+    q = wl.normal_bf16(rng, (3, N_Q, D))
+    ws = pk.decode_workspace_q8(3, table.shape[2])
+    pk.pa_decode_set_test_fault(0, 50_000)
+    try:
+        _, err = _decode(q, pool, scales, table, lens, ws=ws)
+    finally:
+        pk.pa_decode_set_test_fault(-1)
+    assert err & 16
+    ref, _ = oracle.decode_attention(q, q8.pool_bf16(pool, scales), table, lens, 0)
+    got, err = _decode(q, pool, scales, table, lens, ws=ws)
+    assert err == 0
+    _assert_close(got, ref, q, pool, scales, 900, 0.125, 2.0 ** -12)
+
+
 # ------------------------------------------------------------------- append
 class _State:
     def __init__(self, pool, scales, table, fl, fc):
