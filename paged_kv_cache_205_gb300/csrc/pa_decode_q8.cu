@@ -12,21 +12,32 @@
 // registers and two tiles ahead, reached 2.9 TB/s of the copy peak's 6.8 on 256
 // ragged sequences: each chunk's first loads waited for its page ids.)
 //
-// A consumer's inner and output dimensions are permuted to what wide
-// shared-memory loads deliver (a sum may be taken in any order):
-//   S = Q K^T  lane (g, c) (g = lane / 4, c = lane % 4) reads dims 16c..16c+15
-//              of tokens g and g + 8 (one 16-byte load each); k-step ks of
-//              the m16n8k16 MMAs takes dims 16c + 4 ks + {0, 1} and {2, 3}.
-//   O = P V    ldmatrix.trans on byte pairs: a register holds dims 2g, 2g + 1
-//              of a 16-dim group for tokens 2c, 2c + 1; one byte permute and
-//              two conversions make the B operands of two MMAs, whose columns
-//              are the group's even and odd dims.
+// A consumer computes the transposed products, so that the 4 q heads of the
+// group fill half of the MMAs' 8 columns (as rows they would fill a quarter of
+// 16): S^T = K Q^T (tokens x heads, 4 m16n8k16) and O^T = V^T P^T (dims x
+// heads, 4 m16n8k16) a tile.  The inner and output dimensions are permuted to
+// what wide shared-memory loads deliver (a sum may be taken in any order):
+//   S^T  lane (g, c) (g = lane / 4, c = lane % 4) reads dims 16c..16c+15 of
+//        the tokens that rows g and g + 8 stand for (one 16-byte load each);
+//        k-step ks takes dims 16c + 4 ks + {0, 1} and {2, 3}.
+//   P    S^T's fragments in f16 become P^T's with one movmatrix per 8 tokens.
+//   O^T  ldmatrix.trans on byte pairs: a register holds dims 2g, 2g + 1 of a
+//        16-dim group for two tokens; one byte permute and two conversions
+//        make A's rows g (even dims) and g + 8 (odd dims).
+//   Row n of a group of 8 stands for token n / 2 + 4 (n % 2): with two heads'
+//   64 bytes in a 128-byte row, swizzled by the token, the loads of both
+//   products are then free of bank conflicts.
+// The running maximum is a reference that moves only when a score exceeds it
+// by more than 2^8 (one vote a tile instead of a reduction over the tokens and
+// a rescale of O), so P <= 2^8.
+// The copies' rows are two heads wide (128 bytes) because the TMA unit takes a
+// box row by row: with 64-byte rows (one head) 4 x 32768 tokens took 37.7 us.
 // e4m3 becomes f16 exactly; q is scaled by a power of two per head to f16
-// (exact for values down to 2^-29 of the head's largest).  P <= 1 enters the
-// MMA in f16: half a step is 2^-12 of a weight (2^-25 absolute below 2^-14),
-// an eighth of the output's own bf16 rounding; m and l stay fp32.  K's scale
+// (exact for values down to 2^-29 of the head's largest).  P enters the MMA in
+// f16: half a step is 2^-12 of a weight (2^-25 absolute below 2^-14), an
+// eighth of the output's own bf16 rounding; m and l stay fp32.  K's scale
 // multiplies the scores; V's multiplies the tile's product when it is added
-// to the running output, in the FMA that rescales it anyway.
+// to the running output.
 #include <climits>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -48,6 +59,9 @@ constexpr int kMaxGrid = 512;
 constexpr int kChunksPerCta = 4;           // average chunks a CTA takes
 constexpr int kTile = 16;                  // tokens
 constexpr int kTileBytes = 2 * kTile * kQ8TokBytes;   // K and V of 8 heads: 16 KiB
+constexpr int kPairBytes = 2 * kQ8HeadBytes;          // one token, two heads: a row of the copies
+constexpr float kNoScore = -1e30f;       // the reference before a score is seen
+constexpr float kMove = 8.f;             // log2 units a score may lie above the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int kSegStart = 1;   // first tile of a (chunk, sequence) piece
@@ -88,8 +102,8 @@ struct Q8DecodeParams {
 };
 
 struct __align__(1024) Smem {
-  unsigned char kv[kStages][kTileBytes];   // [K|V][head][16 tokens][64], 64-byte swizzled; 8-token
-                                           // pages: two of [K|V][head][8][64]
+  unsigned char kv[kStages][kTileBytes];   // [K|V][head pair][16 tokens][2][64], 128-byte swizzled;
+                                           // 8-token pages: two of [K|V][pair][8][2][64]
   float scale[kStages][2][2 * kHkv];       // [page of the tile][K|V][head]
   int prefix[kMaxSeqs + 1];                // tiles of sequences 0..s-1
   StageDesc desc[kStages];
@@ -98,22 +112,36 @@ struct __align__(1024) Smem {
   int warp_sum[kWarps];
 };
 
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a2, uint32_t b0,
-                                              uint32_t b1) {
-  // rows 8..15 of A are zero
+// D = A B + D and D = A B, m16n8k16 and m16n8k8, f16 in, fp32 out.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(0u), "r"(a2), "r"(0u), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-__device__ __forceinline__ void mma_f16_1688(float (&d)[4], uint32_t a0, uint32_t b0) {
+__device__ __forceinline__ void mma_16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_1688_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(0u), "r"(b0));
+      "{%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
+}
+
+// The transpose of an 8 x 8 matrix of f16 held as an MMA fragment.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Packed two-lane fp32 product.
@@ -147,26 +175,24 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A warp's running softmax of one kv head: q head g (rows g < 4 are real),
-// dims 16 i + 4c + {0, 2} (o[2 i]) and {1, 3} (o[2 i + 1]).
+// A warp's running softmax of one kv head.  Lane (g, c) holds q heads 2c and
+// 2c + 1 of the group (lanes c < 2; the others compute columns of zeros):
+// dims 16 i + 2 g (o[2 i]) and 16 i + 2 g + 1 (o[2 i + 1]) of both, and the sums over its
+// own tokens.
 struct State {
   float2 o[8];
-  float m, l;
+  float2 m, l;   // m (log2 domain) is the same in the 8 lanes of a head pair
   __device__ __forceinline__ void reset() {
-    m = neg_inf();
-    l = 0.f;
+    m = make_float2(kNoScore, kNoScore);
+    l = make_float2(0.f, 0.f);
 #pragma unroll
     for (int t = 0; t < 8; ++t) o[t] = make_float2(0.f, 0.f);
-  }
-  // dims 16 i + 4c .. + 3
-  __device__ __forceinline__ float4 dims(int i) const {
-    return make_float4(o[2 * i].x, o[2 * i + 1].x, o[2 * i].y, o[2 * i + 1].y);
   }
 };
 
 // q head g of the group in f16, scaled by a power of two to [2^12, 2^13);
-// returns the row's score factor: qscale / that power.  Lane c holds dims
-// 16c .. 16c+15 (the order of the K loads).
+// returns the head's score factor: qscale / that power.  Lane c holds dims
+// 16c .. 16c+15 (the order of the K loads): B's columns of S^T.
 __device__ __forceinline__ float load_q(const uint16_t *q_token, int head0, int g, int c,
                                         float qscale, uint32_t (&qa)[8]) {
   uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
@@ -191,83 +217,97 @@ __device__ __forceinline__ float load_q(const uint16_t *q_token, int head0, int 
   return qscale * down;
 }
 
-// Folds a tile into the state.  k0 / k1: the head's K rows of tokens 0..7 and
-// 8..15 in shared memory, v0 / v1 its V rows.  use: tokens to use (not 0).
+// Folds a tile into the state.  k0 / k1: the head pair's K rows of tokens 0..7
+// and 8..15 in shared memory, v0 / v1 its V rows; chunk0: the head's first
+// 16-byte chunk of a row (0 or 4).  use: tokens to use (not 0).
 template <int BT>
 __device__ __forceinline__ void attend(uint32_t k0, uint32_t k1, uint32_t v0, uint32_t v1,
-                                       float2 sk, float2 sv, uint32_t use, const uint32_t (&qa)[8],
-                                       float qs, int lane, State &st) {
+                                       int chunk0, float2 sk, float2 sv, uint32_t use,
+                                       const uint32_t (&qa)[8], float2 qs, int lane, State &st) {
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t koff = g * kQ8HeadBytes + ((c ^ ((g >> 1) & 3)) << 4);
+  const int kt = (g >> 1) + 4 * (g & 1);   // the token of column g
+  const uint32_t koff = kt * kPairBytes + (((chunk0 + c) ^ kt) << 4);
   const uint4 ka = lds16(k0 + koff), kb = lds16(k1 + koff);
-  const int r = lane & 7;
-  const uint32_t voff = r * kQ8HeadBytes + (((lane >> 3) ^ ((r >> 1) & 3)) << 4);
+  const int vt = ((lane & 7) >> 1) + 4 * (lane & 1);
+  const uint32_t voff = vt * kPairBytes + (((chunk0 + (lane >> 3)) ^ vt) << 4);
   uint32_t va[4], vb[4];
   ldsm_x4_trans(v0 + voff, va[0], va[1], va[2], va[3]);
   ldsm_x4_trans(v1 + voff, vb[0], vb[1], vb[2], vb[3]);
-  bool u[4] = {true, true, true, true};
   if (use != 0xffffu) {
-    // unused tokens may hold anything, NaN included: they meet P = 0
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = (use >> (2 * c + (i & 1) + 8 * (i >> 1))) & 1u;
-    const uint32_t ma = (u[0] ? 0xffffu : 0u) | (u[1] ? 0xffff0000u : 0u);
-    const uint32_t mb = (u[2] ? 0xffffu : 0u) | (u[3] ? 0xffff0000u : 0u);
+    // unused tokens may hold anything, NaN included: they meet P = 0.  (V's
+    // registers hold tokens c and c + 4 of each group of 8.)
+    const uint32_t ma = ((use >> c) & 1u ? 0xffffu : 0u) | ((use >> (c + 4)) & 1u ? 0xffff0000u : 0u);
+    const uint32_t mb = ((use >> (c + 8)) & 1u ? 0xffffu : 0u) | ((use >> (c + 12)) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       va[i] &= ma;
       vb[i] &= mb;
     }
   }
-  // ---- S = Q K^T for tokens 0..7 (s0) and 8..15 (s1)
-  float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+  // ---- S^T = K Q^T: s[0], s[1] = heads 2c, 2c + 1 of row g's token, s[2], s[3] of row g + 8's
+  float s[4];
   const uint32_t kw0[4] = {ka.x, ka.y, ka.z, ka.w}, kw1[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
-    mma_f16_16816(s0, qa[2 * ks], qa[2 * ks + 1], e4m3x2_to_f16x2(kw0[ks]),
-                  e4m3x2_to_f16x2(kw0[ks] >> 16));
-    mma_f16_16816(s1, qa[2 * ks], qa[2 * ks + 1], e4m3x2_to_f16x2(kw1[ks]),
-                  e4m3x2_to_f16x2(kw1[ks] >> 16));
+    const uint32_t a[4] = {e4m3x2_to_f16x2(kw0[ks]), e4m3x2_to_f16x2(kw1[ks]),
+                           e4m3x2_to_f16x2(kw0[ks] >> 16), e4m3x2_to_f16x2(kw1[ks] >> 16)};
+    if (ks == 0) mma_16816_zero(s, a, qa[0], qa[1]);
+    else mma_16816(s, a, qa[2 * ks], qa[2 * ks + 1]);
   }
-  // ---- online softmax of row g over tokens 2c, 2c+1, 2c+8, 2c+9
-  const float f0 = qs * sk.x, f1 = BT == 8 ? qs * sk.y : f0;
-  const float x0 = u[0] ? s0[0] * f0 : neg_inf();
-  const float x1 = u[1] ? s0[1] * f0 : neg_inf();
-  const float x2 = u[2] ? s1[0] * f1 : neg_inf();
-  const float x3 = u[3] ? s1[1] * f1 : neg_inf();
-  float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  const float m_new = fmaxf(st.m, mx);
-  const float base = m_new == neg_inf() ? 0.f : m_new;   // nothing seen yet
-  const float alpha = fast_exp2(st.m - base);
-  const float p0 = fast_exp2(x0 - base), p1 = fast_exp2(x1 - base);
-  const float p2 = fast_exp2(x2 - base), p3 = fast_exp2(x3 - base);
-  st.l = fmaf(st.l, alpha, (p0 + p1) + (p2 + p3));
-  st.m = m_new;
-  const uint32_t pa = f16x2(p0, p1), pc = f16x2(p2, p3);
-  // ---- O = alpha O + sV P V, 16 dims a step: the even ones, the odd ones
-  const float2 al = make_float2(alpha, alpha);
+  // ---- scores against the reference (log2 domain)
+  const float2 f0 = make_float2(qs.x * sk.x, qs.y * sk.x);
+  const float2 f1 = BT == 8 ? make_float2(qs.x * sk.y, qs.y * sk.y) : f0;
+  // (the product is rounded before the reference is taken off: a fused
+  // x - m would leave m's rounding error, which for scores of 2^28 and more
+  // overflows the exponential)
+  float2 x0 = mul2(make_float2(s[0], s[1]), f0), x1 = mul2(make_float2(s[2], s[3]), f1);
+  if (use != 0xffffu) {   // (K rows of unused tokens may hold anything too)
+    if (!((use >> kt) & 1u)) x0 = make_float2(neg_inf(), neg_inf());
+    if (!((use >> (kt + 8)) & 1u)) x1 = make_float2(neg_inf(), neg_inf());
+  }
+  float over = fmaxf(fmaxf(x0.x, x1.x) - st.m.x, fmaxf(x0.y, x1.y) - st.m.y);
+  if (__any_sync(0xffffffffu, over > kMove)) {
+    // the reference moves to the largest score so far
+    float nx = fmaxf(x0.x, x1.x), ny = fmaxf(x0.y, x1.y);
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, d));
+      ny = fmaxf(ny, __shfl_xor_sync(0xffffffffu, ny, d));
+    }
+    nx = fmaxf(nx, st.m.x);
+    ny = fmaxf(ny, st.m.y);
+    const float2 al = make_float2(fast_exp2(st.m.x - nx), fast_exp2(st.m.y - ny));
+    st.m = make_float2(nx, ny);
+    st.l = mul2(st.l, al);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st.o[i] = mul2(st.o[i], al);
+  }
+  const float y0 = x0.x - st.m.x, y1 = x0.y - st.m.y, y2 = x1.x - st.m.x, y3 = x1.y - st.m.y;
+  const float p0 = fast_exp2(y0), p1 = fast_exp2(y1), p2 = fast_exp2(y2), p3 = fast_exp2(y3);
+  st.l.x += p0 + p2;
+  st.l.y += p1 + p3;
+  const uint32_t b0 = transpose8x8(f16x2(p0, p1)), b1 = transpose8x8(f16x2(p2, p3));
+  // ---- O^T += sV V^T P^T, 16 dims a step
   const float2 sv0 = make_float2(sv.x, sv.x), sv1 = make_float2(sv.y, sv.y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // bytes (t0 d0, t0 d1, t1 d0, t1 d1) to (t0 d0, t1 d0, t0 d1, t1 d1)
-    const uint32_t a = prmt(va[i], 0u, 0x3120), b = prmt(vb[i], 0u, 0x3120);
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd) {
-      const uint32_t b0 = e4m3x2_to_f16x2(a >> (16 * odd)), b1 = e4m3x2_to_f16x2(b >> (16 * odd));
-      float2 &o = st.o[2 * i + odd];
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      if (BT == 8) {
-        // the two pages' products apart: their scales differ
-        float d2[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16_1688(d, pa, b0);
-        mma_f16_1688(d2, pc, b1);
-        o = fma2(make_float2(d2[0], d2[1]), sv1, fma2(make_float2(d[0], d[1]), sv0, mul2(o, al)));
-      } else {
-        mma_f16_16816(d, pa, pc, b0, b1);
-        o = fma2(make_float2(d[0], d[1]), sv0, mul2(o, al));
-      }
+    const uint32_t x = prmt(va[i], 0u, 0x3120), z = prmt(vb[i], 0u, 0x3120);
+    const uint32_t a[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(z),
+                           e4m3x2_to_f16x2(z >> 16)};
+    float d[4];
+    if (BT == 8) {
+      // the two pages' products apart: their scales differ
+      float d2[4];
+      mma_1688_zero(d, a[0], a[1], b0);
+      mma_1688_zero(d2, a[2], a[3], b1);
+      st.o[2 * i] = fma2(make_float2(d2[0], d2[1]), sv1, st.o[2 * i]);
+      st.o[2 * i + 1] = fma2(make_float2(d2[2], d2[3]), sv1, st.o[2 * i + 1]);
+    } else {
+      mma_16816_zero(d, a, b0, b1);
     }
+    st.o[2 * i] = fma2(make_float2(d[0], d[1]), sv0, st.o[2 * i]);
+    st.o[2 * i + 1] = fma2(make_float2(d[2], d[3]), sv0, st.o[2 * i + 1]);
   }
 }
 
@@ -476,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ===================================================== consumer warps ==
     const int g = lane >> 2, c = lane & 3;
     constexpr int kRows = BT == 8 ? 8 : kTile;                  // token rows of a head in a stage
-    constexpr uint32_t kHeadTile = kRows * kQ8HeadBytes;        // one head's K (or V) there
-    constexpr uint32_t kHalf = kHkv * kHeadTile;                // V behind K
-    constexpr uint32_t kSecond = BT == 8 ? kTileBytes / 2 : 8 * kQ8HeadBytes;   // tokens 8..15
+    constexpr uint32_t kPairTile = kRows * kPairBytes;          // a head pair's K (or V) there
+    constexpr uint32_t kHalf = kHkv / 2 * kPairTile;            // V behind K
+    constexpr uint32_t kSecond = BT == 8 ? kTileBytes / 2 : 8 * kPairBytes;   // tokens 8..15
     uint32_t qa[8];
-    float qs = 0.f;
+    float2 qs = make_float2(0.f, 0.f);
     State st;
     st.reset();
 #pragma unroll
@@ -495,11 +535,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const StageDesc d = sm.desc[stage];
       if (d.flags & kEndOfWork) break;
       if (d.flags & kSegStart) {
-        qs = load_q(p.q + static_cast<size_t>(d.seq) * kHq * kD, warp * kGqa, g, c, p.qscale, qa);
+        const float mine = load_q(p.q + static_cast<size_t>(d.seq) * kHq * kD, warp * kGqa, g, c,
+                                  p.qscale, qa);
+        qs.x = __shfl_sync(0xffffffffu, mine, 8 * c);       // heads 2c, 2c + 1
+        qs.y = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
         st.reset();
       }
       if (d.use) {
-        const uint32_t k0 = smem_u32(sm.kv[stage]) + warp * kHeadTile;
+        const uint32_t k0 = smem_u32(sm.kv[stage]) + (warp >> 1) * kPairTile;
         const float(&sc)[2][2 * kHkv] = sm.scale[stage];
         float2 sk, sv;
         sk.x = sc[0][warp];
@@ -513,33 +556,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             sv.y = sc[1][kHkv + warp];
           }
         }
-        attend<BT>(k0, k0 + kSecond, k0 + kHalf, k0 + kHalf + kSecond, sk, sv, d.use, qa, qs, lane,
-                   st);
+        attend<BT>(k0, k0 + kSecond, k0 + kHalf, k0 + kHalf + kSecond, 4 * (warp & 1), sk, sv, d.use,
+                   qa, qs, lane, st);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[stage]);
       if (d.flags & kSegEnd) {
         // ---- finish this piece of sequence d.seq
-        float lt = st.l;
-        lt += __shfl_xor_sync(0xffffffffu, lt, 1);
-        lt += __shfl_xor_sync(0xffffffffu, lt, 2);
-        if (g < kGqa) {
-          const int h = warp * kGqa + g;
+        float2 lt = st.l;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          lt.x += __shfl_xor_sync(0xffffffffu, lt.x, x);
+          lt.y += __shfl_xor_sync(0xffffffffu, lt.y, x);
+        }
+        if (c < kGqa / 2) {
+          const int h = warp * kGqa + 2 * c;   // and h + 1
           if (d.slot < 0) {
-            const float inv = lt == 0.f ? 0.f : 1.f / lt;   // 0: no page of the context is valid
-            uint2 *dst = reinterpret_cast<uint2 *>(p.out + (static_cast<size_t>(d.seq) * kHq + h) * kD + 4 * c);
+            // 0: no page of the context is valid
+            const float ix = lt.x == 0.f ? 0.f : 1.f / lt.x, iy = lt.y == 0.f ? 0.f : 1.f / lt.y;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(
+                p.out + (static_cast<size_t>(d.seq) * kHq + h) * kD) + g;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float4 o = st.dims(i);
-              dst[4 * i] = make_uint2(float2_to_bf16x2(o.x * inv, o.y * inv),
-                                      float2_to_bf16x2(o.z * inv, o.w * inv));
+              dst[8 * i] = float2_to_bf16x2(st.o[2 * i].x * ix, st.o[2 * i + 1].x * ix);
+              dst[8 * i + kD / 2] = float2_to_bf16x2(st.o[2 * i].y * iy, st.o[2 * i + 1].y * iy);
             }
           } else {
             const size_t at = static_cast<size_t>(d.slot) * kHq + h;
-            float4 *dst = reinterpret_cast<float4 *>(p.acc + at * kD + 4 * c);
+            float2 *dst = reinterpret_cast<float2 *>(p.acc + at * kD) + g;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[4 * i] = st.dims(i);
-            if (c == 0) p.ml[at] = make_float2(st.m, lt);
+            for (int i = 0; i < 4; ++i) {
+              dst[8 * i] = make_float2(st.o[2 * i].x, st.o[2 * i + 1].x);
+              dst[8 * i + kD / 2] = make_float2(st.o[2 * i].y, st.o[2 * i + 1].y);
+            }
+            if (g == 0) {
+              p.ml[at] = make_float2(st.m.x, lt.x);
+              p.ml[at + 1] = make_float2(st.m.y, lt.y);
+            }
           }
         }
       }
@@ -634,10 +687,10 @@ long long slots_for(int num_seqs, int grid) {
   return static_cast<long long>(kChunksPerCta) * grid + 2 + num_seqs;
 }
 
-// Tensor map over the pool: dims (d 64, token bt, kv head 8, K|V 2, block),
-// the token dimension before the head dimension although its stride is the
-// larger one, so that a copy writes each head's token rows together; box
-// (64, 8 or 16, 8, 2, 1), 64-byte swizzle.
+// Tensor map over the pool: dims (two heads' d 128, token bt, head pair 4, K|V
+// 2, block), the token dimension before the pairs although its stride is the
+// larger one, so that a copy writes each pair's token rows together; box
+// (128, 8 or 16, 4, 2, 1), 128-byte swizzle.
 int make_q8_tile_map(CUtensorMap *map, const void *kv_cache, int num_blocks, int bt) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
@@ -650,14 +703,14 @@ int make_q8_tile_map(CUtensorMap *map, const void *kv_cache, int num_blocks, int
     fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   }
   const cuuint64_t half = static_cast<cuuint64_t>(bt) * kQ8TokBytes;
-  const cuuint64_t dims[5] = {kD, static_cast<cuuint64_t>(bt), kHkv, 2,
+  const cuuint64_t dims[5] = {kPairBytes, static_cast<cuuint64_t>(bt), kHkv / 2, 2,
                               static_cast<cuuint64_t>(num_blocks)};
-  const cuuint64_t strides[4] = {kQ8TokBytes, kQ8HeadBytes, half, 2 * half};
-  const cuuint32_t box[5] = {kD, bt == 8 ? 8u : 16u, kHkv, 2, 1};
+  const cuuint64_t strides[4] = {kQ8TokBytes, kPairBytes, half, 2 * half};
+  const cuuint32_t box[5] = {kPairBytes, bt == 8 ? 8u : 16u, kHkv / 2, 2, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(kv_cache), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
 }
