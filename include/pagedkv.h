@@ -601,9 +601,9 @@ int pa_prefill_append_rope_q8(const uint16_t *k_new, const uint16_t *v_new,
  * pa_decode_attention_q8 -- pa_decode_attention over the 8-bit cache: q and
  * out stay bf16, sums and the softmax are fp32.  A sequence with context 0
  * gets a zero output, and so does one none of whose pages is valid.
- * num_seqs is at most 2048.  workspace: pa_decode_workspace_size_q8 bytes,
- * zero-filled once before its first use, not shared by calls that overlap in
- * time; it is not interchangeable with pa_decode_attention's.
+ * num_seqs is at most 2048.  workspace: pa_decode_workspace_size_q8 bytes of
+ * scratch whose contents do not matter; calls that overlap in time must not
+ * share it.
  * pa_decode_set_path and pa_decode_set_grid_limit do not apply.
  */
 int pa_decode_attention_q8(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,

@@ -573,11 +573,11 @@ def pa_decode_workspace_size_q8(num_seqs: int, max_blocks_per_seq: int,
 
 def decode_workspace_q8(num_seqs: int, max_blocks_per_seq: int, device=None,
                         block_tokens: int = PA_BLOCK_TOKENS):
-    """A zero-filled uint8 CUDA tensor of pa_decode_workspace_size_q8 bytes,
-    the state pa_decode_attention_q8 expects on first use."""
+    """A uint8 CUDA tensor of pa_decode_workspace_size_q8 bytes (scratch of
+    pa_decode_attention_q8: its contents do not matter)."""
     torch = _torch()
     n = pa_decode_workspace_size_q8(num_seqs, max_blocks_per_seq, block_tokens)
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
 def pa_decode_attention_q8(out, q, kv_cache, kv_scales, block_table, context_lens, layer, scale,

@@ -3,14 +3,29 @@
 //   out[h] = sum_t softmax_t(scale * q[h] . (sK K_t)) (sV V_t)
 //
 // decode_q8_kernel: the 16-token tiles of all sequences are laid end to end
-// and cut into chunks; a CTA takes its own index first, then chunks from a
-// counter in the workspace.  A producer warp streams tiles into a ring of
-// shared-memory stages, one 16 KiB TMA copy (16 tokens x 8 kv heads x K, V)
-// and one 64-byte copy of the page's scales a tile, and runs ahead over chunk
-// and sequence borders; eight consumer warps, one per kv head, follow.
-// (Tiles loaded by the consumer warps themselves, straight into the MMAs'
-// registers and two tiles ahead, reached 2.9 TB/s of the copy peak's 6.8 on 256
-// ragged sequences: each chunk's first loads waited for its page ids.)
+// and cut into one equal run for each CTA (two CTAs an SM).  A producer warp
+// streams the run's tiles into a ring of shared-memory stages, one 16 KiB TMA
+// copy (16 tokens x 8 kv heads x K, V) and one 64-byte copy of the page's
+// scales a tile, and the sequence's q with the first tile of a piece; eight
+// consumer warps, one per kv head, follow.  A sequence that lies in one run
+// is written by its CTA; the pieces of the others are merged by
+// decode_q8_merge_kernel.  Tables of at most kDirectTiles tiles a sequence run
+// one CTA a sequence and no merge.
+// Measured on the way (us, 4 x 32768 tokens / 256 ragged sequences; floors at
+// the copy peak 19.8 / 39.1):
+//   46.1 / 92.8  consumer warps load tiles into registers, two ahead: each
+//                chunk's first loads wait for its page ids
+//   36.1 / 64.1  the producer warp; chunks of 1/4 of a CTA's share from a counter
+//   33.2 / 63.2  q with the tiles, page ids a batch ahead, half a share a chunk
+//   29.2 / 52.8  one run a CTA: the finer cuts balance SMs of unequal speed
+//                better (the last tile at 45.9 instead of 47.3 us), but every
+//                piece costs 8.4 KiB of partial written and read again
+//   26.9 / 53.5  the plan made, and 4 tiles a CTA prefetched, while the kernels
+//                before end (2 rows of 14 to 17 tokens, direct: 5.5 to 3.5)
+// Of the 53.5: 4.4 to the first data, 37 at 7.1 TB/s, 5 between the CTAs' last
+// tiles (SMs of unequal speed), 5 to end, launch and run the merge.
+// The copies' rows are two heads wide (128 bytes): the TMA unit takes a box row
+// by row.
 //
 // A consumer computes the transposed products, so that the 4 q heads of the
 // group fill half of the MMAs' 8 columns (as rows they would fill a quarter of
@@ -30,8 +45,6 @@
 // The running maximum is a reference that moves only when a score exceeds it
 // by more than 2^8 (one vote a tile instead of a reduction over the tokens and
 // a rescale of O), so P <= 2^8.
-// The copies' rows are two heads wide (128 bytes) because the TMA unit takes a
-// box row by row: with 64-byte rows (one head) 4 x 32768 tokens took 37.7 us.
 // e4m3 becomes f16 exactly; q is scaled by a power of two per head to f16
 // (exact for values down to 2^-29 of the head's largest).  P enters the MMA in
 // f16: half a step is 2^-12 of a weight (2^-25 absolute below 2^-14), an
@@ -53,18 +66,19 @@ constexpr int kWarps = kHkv;               // consumer warps, one per kv head
 constexpr int kThreads = (kWarps + 1) * 32;   // + producer warp
 constexpr int kScanThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 6;
-constexpr int kMaxSeqs = 2048;             // tile prefix kept in shared memory
+constexpr int kStages = 5;
+constexpr int kMaxSeqs = 2048;             // the tile prefix is kept in shared memory
 constexpr int kMaxGrid = 512;
-constexpr int kChunksPerCta = 4;           // average chunks a CTA takes
 constexpr int kTile = 16;                  // tokens
+constexpr int kDirectTiles = 8;            // longest table served by one CTA a sequence
+constexpr int kPrefetchTiles = 4;          // tiles brought into L2 before the wait
 constexpr int kTileBytes = 2 * kTile * kQ8TokBytes;   // K and V of 8 heads: 16 KiB
 constexpr int kPairBytes = 2 * kQ8HeadBytes;          // one token, two heads: a row of the copies
 constexpr float kNoScore = -1e30f;       // the reference before a score is seen
 constexpr float kMove = 8.f;             // log2 units a score may lie above the reference
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kSegStart = 1;   // first tile of a (chunk, sequence) piece
+constexpr int kSegStart = 1;   // first tile of a sequence's piece in the run
 constexpr int kSegEnd = 2;     // last tile of that piece
 constexpr int kEndOfWork = 4;  // no more tiles; the stage carries no data
 
@@ -82,8 +96,7 @@ struct Q8DecodeParams {
   const float *scales;
   const int32_t *block_table;
   const int32_t *context_lens;
-  int *chunk_counter;  // zero between calls; reset by the merge kernel
-  int2 *meta;          // [num_seqs] (first partial slot, number of partials)
+  // partials: the piece of sequence s in run k is slot k + s
   float2 *ml;          // [slots][32] (m, l), m in the log2 domain
   float *acc;          // [slots][32][64] unnormalised output
   int32_t *err;
@@ -94,7 +107,7 @@ struct Q8DecodeParams {
   int layer;
   int cap_tokens;
   float qscale;        // scale * log2(e)
-  long long n_slots;
+  int direct;          // one CTA a sequence
   // test hook (pa_decode_set_test_fault): the stage of CTA 0 whose copies are
   // left out (-1: none), and the limit of every wait
   int fault_stage;
@@ -104,12 +117,13 @@ struct Q8DecodeParams {
 struct __align__(1024) Smem {
   unsigned char kv[kStages][kTileBytes];   // [K|V][head pair][16 tokens][2][64], 128-byte swizzled;
                                            // 8-token pages: two of [K|V][pair][8][2][64]
+  unsigned char q[kStages][kHq * kD * 2];  // first tile of a piece: the sequence's q
   float scale[kStages][2][2 * kHkv];       // [page of the tile][K|V][head]
-  int prefix[kMaxSeqs + 1];                // tiles of sequences 0..s-1
   StageDesc desc[kStages];
   uint64_t full[kStages];
   uint64_t empty[kStages];
   int warp_sum[kWarps];
+  int prefix[1];                           // [num_seqs + 1] tiles of sequences 0..s-1
 };
 
 // D = A B + D and D = A B, m16n8k16 and m16n8k8, f16 in, fp32 out.
@@ -192,14 +206,15 @@ struct State {
 
 // q head g of the group in f16, scaled by a power of two to [2^12, 2^13);
 // returns the head's score factor: qscale / that power.  Lane c holds dims
-// 16c .. 16c+15 (the order of the K loads): B's columns of S^T.
-__device__ __forceinline__ float load_q(const uint16_t *q_token, int head0, int g, int c,
-                                        float qscale, uint32_t (&qa)[8]) {
+// 16c .. 16c+15 (the order of the K loads): B's columns of S^T.  q_group: the
+// group's q in shared memory.
+__device__ __forceinline__ float load_q(uint32_t q_group, int g, int c, float qscale,
+                                        uint32_t (&qa)[8]) {
   uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
   if (g < kGqa) {
-    const uint4 *row = reinterpret_cast<const uint4 *>(q_token + (head0 + g) * kD + 16 * c);
-    w0 = row[0];
-    w1 = row[1];
+    const uint32_t at = q_group + (g * kD + 16 * c) * 2;
+    w0 = lds16(at);
+    w1 = lds16(at + 16);
   }
   const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
   uint32_t top = 0;
@@ -311,28 +326,81 @@ __device__ __forceinline__ void attend(uint32_t k0, uint32_t k1, uint32_t v0, ui
   }
 }
 
-__device__ __forceinline__ int clamped_ctx(const Q8DecodeParams &p, int s) {
-  return min(max(p.context_lens[s], 0), p.cap_tokens);
+// Context lengths and page ids are read past L1: they may be read before the
+// wait on the kernels before (to know what to prefetch) and again after it.
+__device__ __forceinline__ int ctx_now(const Q8DecodeParams &p, int s) {
+  return __ldcg(p.context_lens + s);
 }
-
-// Chunk length in tiles: about kChunksPerCta chunks per CTA, at least 8
-// tiles (or one CTA's fair share when that is smaller).
-__device__ __forceinline__ int chunk_tiles(int total, int g) {
-  const int fair = (total + g - 1) / g;
-  const int c = (total + kChunksPerCta * g - 1) / (kChunksPerCta * g);
-  return max(1, max(min(8, fair), c));
+__device__ __forceinline__ int clamp_ctx(const Q8DecodeParams &p, int t) {
+  return min(max(t, 0), p.cap_tokens);
 }
+__device__ __forceinline__ int tiles_in(int ctx) { return (ctx + kTile - 1) / kTile; }
 
-// First sequence s with prefix[s+1] > b or prefix[s] >= b (one that reaches
-// past tile b, or an empty one starting at b or later).
-__device__ __forceinline__ int first_seq_at(const int *prefix, int n, int b) {
-  int lo = 0, hi = n;
+// Sequence holding tile b (b < total): the smallest s with prefix[s+1] > b.
+__device__ __forceinline__ int seq_of_tile(const int *prefix, int n, int b) {
+  int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (prefix[mid + 1] > b || prefix[mid] >= b) hi = mid;
+    if (prefix[mid + 1] > b) hi = mid;
     else lo = mid + 1;
   }
   return lo;
+}
+
+// A tile as the producer's lane that issues it knows it.
+struct TileWork {
+  int blk, blk2;   // page ids (blk2: second page of a tile over 8-token pages, -2: there is none)
+  int j;           // tile of the sequence
+  int n_tok;
+  StageDesc d;     // (d.use is set when the tile is issued)
+};
+
+// Lane i: tile t + i of the CTA's run [b0, b1).  Its page ids are read here
+// and first looked at when the tile is issued.
+template <int BT>
+__device__ __forceinline__ TileWork tile_work(const Q8DecodeParams &p, const Smem &sm, int t, int b0,
+                                              int b1, int lane) {
+  TileWork w;
+  w.blk = -1;
+  w.blk2 = -2;
+  w.j = w.n_tok = 0;
+  w.d.seq = w.d.flags = 0;
+  w.d.slot = -1;
+  w.d.use = 0;
+  const int b = t + lane;
+  if (b < b1) {
+    const int s = p.direct ? static_cast<int>(blockIdx.x) : seq_of_tile(sm.prefix, p.num_seqs, b);
+    const int B = p.direct ? 0 : sm.prefix[s], E = p.direct ? b1 : sm.prefix[s + 1];
+    w.j = b - B;
+    const int32_t *row =
+        p.block_table + (static_cast<size_t>(s) * p.n_layers + p.layer) * p.max_blocks;
+    w.blk = __ldcg(row + (BT == 32 ? w.j >> 1 : BT == 8 ? 2 * w.j : w.j));
+    w.n_tok = kTile;
+    if (b == E - 1) w.n_tok = clamp_ctx(p, ctx_now(p, s)) - w.j * kTile;
+    if (BT == 8 && w.n_tok > 8) w.blk2 = __ldcg(row + 2 * w.j + 1);
+    w.d.seq = s;
+    w.d.flags = (w.j == 0 || b == b0 ? kSegStart : 0) | (b == E - 1 || b == b1 - 1 ? kSegEnd : 0);
+    if (B < b0 || E > b1) w.d.slot = blockIdx.x + s;   // the sequence is cut into several pieces
+  }
+  return w;
+}
+
+// Brings a tile into L2.
+template <int BT>
+__device__ __forceinline__ void prefetch_tile(const Q8DecodeParams &p, const TileWork &w) {
+  constexpr size_t kPage = static_cast<size_t>(BT) * 2 * kQ8TokBytes;
+  if (w.blk < 0 || w.blk >= p.num_blocks) return;
+  const unsigned char *page = p.kv + static_cast<size_t>(w.blk) * kPage;
+  if (BT == 32) {
+    page += (w.j & 1) * (kTile * kQ8TokBytes);
+    prefetch_bulk_l2(page, kTile * kQ8TokBytes);
+    prefetch_bulk_l2(page + kPage / 2, kTile * kQ8TokBytes);
+  } else {
+    prefetch_bulk_l2(page, kPage);
+    if (BT == 8 && w.blk2 >= 0 && w.blk2 < p.num_blocks)
+      prefetch_bulk_l2(p.kv + static_cast<size_t>(w.blk2) * kPage, kPage);
+  }
+  prefetch_l2(p.scales + static_cast<size_t>(w.blk) * 2 * kHkv);
 }
 
 // Tile prefix over the sequences into sm.prefix; returns the total.  Every
@@ -343,11 +411,7 @@ __device__ __forceinline__ int tile_prefix(const Q8DecodeParams &p, Smem &sm, in
   for (int base = 0; base < p.num_seqs; base += kScanThreads) {
     const int i = base + tid;
     int nb = 0;
-    if (tid < kScanThreads && i < p.num_seqs) {
-      const int t = p.context_lens[i];
-      if (blockIdx.x == 0 && (t < 0 || t > p.cap_tokens)) report(p.err, PA_DEV_CTX_RANGE);
-      nb = (clamped_ctx(p, i) + kTile - 1) / kTile;
-    }
+    if (tid < kScanThreads && i < p.num_seqs) nb = tiles_in(clamp_ctx(p, ctx_now(p, i)));
     int incl = nb;
     if (tid < kScanThreads) {
 #pragma unroll
@@ -374,6 +438,13 @@ __device__ __forceinline__ int tile_prefix(const Q8DecodeParams &p, Smem &sm, in
   return carry;
 }
 
+// The CTA's run of tiles.
+__device__ __forceinline__ void run_of(int total, int G, int *b0, int *b1) {
+  const int C = max((total + G - 1) / G, 1);
+  *b0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * C, static_cast<long long>(total)));
+  *b1 = min(total, *b0 + C);
+}
+
 template <int BT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_q8_kernel(const __grid_constant__ CUtensorMap kv_map, Q8DecodeParams p) {
@@ -390,109 +461,113 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     fence_mbar_init();
   }
-  pdl_wait_primary();        // everything read below may come from the previous kernel
-  pdl_launch_dependents();   // the merge kernel may take its place in the queue
-  const int total = tile_prefix(p, sm, tid, warp, lane);
-  const int C = chunk_tiles(total, G);
-  const int n_chunks = max(1, (total + C - 1) / C);
+  int b0 = 0, b1 = 0;
+  TileWork w;
+  if (p.direct) {
+    pdl_wait_primary();        // everything read below may come from the previous kernel
+    pdl_launch_dependents();
+    const int ctx = ctx_now(p, blockIdx.x);
+    if (tid == 0 && (ctx < 0 || ctx > p.cap_tokens)) report(p.err, PA_DEV_CTX_RANGE);
+    b1 = tiles_in(clamp_ctx(p, ctx));
+    if (b1 == 0) {
+      uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(blockIdx.x) * kHq * kD);
+      for (int e = tid; e < kHq * kD * 2 / 16; e += kThreads) o[e] = make_uint4(0, 0, 0, 0);
+    }
+    if (warp == kWarps) w = tile_work<BT>(p, sm, 0, 0, b1, lane);
+    __syncthreads();           // the barriers are initialised
+  } else {
+    // ---- while the kernels before end: a plan from the lengths and page ids
+    // as they read now, which may still change, to bring the run's first tiles
+    // into L2.  Nothing else is done with it unless it still holds afterwards.
+    int total = tile_prefix(p, sm, tid, warp, lane);
+    run_of(total, G, &b0, &b1);
+    if (warp == kWarps) {
+      w = tile_work<BT>(p, sm, b0, b0, b1, lane);
+      if (lane < kPrefetchTiles) prefetch_tile<BT>(p, w);
+    }
+    pdl_wait_primary();        // everything read below is current
+    pdl_launch_dependents();   // the merge kernel may take its place in the queue
+    if (warp == kWarps) w = tile_work<BT>(p, sm, b0, b0, b1, lane);
+    int changed = 0;
+    for (int i = tid; i < p.num_seqs; i += kThreads) {
+      const int t = ctx_now(p, i);
+      if (blockIdx.x == 0 && (t < 0 || t > p.cap_tokens)) report(p.err, PA_DEV_CTX_RANGE);
+      changed |= tiles_in(clamp_ctx(p, t)) != sm.prefix[i + 1] - sm.prefix[i];
+    }
+    if (__syncthreads_or(changed)) {
+      total = tile_prefix(p, sm, tid, warp, lane);
+      run_of(total, G, &b0, &b1);
+      if (warp == kWarps) w = tile_work<BT>(p, sm, b0, b0, b1, lane);
+    }
+    // the CTAs' share of zeros for the sequences with an empty context
+    for (int s = blockIdx.x; s < p.num_seqs; s += G)
+      if (sm.prefix[s] == sm.prefix[s + 1]) {
+        uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(s) * kHq * kD);
+        for (int e = tid; e < kHq * kD * 2 / 16; e += kThreads) o[e] = make_uint4(0, 0, 0, 0);
+      }
+  }
 
   if (warp == kWarps) {
     // ===================================================== producer warp ==
+    // Batches of up to 32 tiles, whatever sequences they belong to: lane i
+    // works out tile i and later issues it.  The next batch's page ids are on
+    // their way while a batch is issued.
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     uint32_t issued = 0, issued_parity = 0;   // per stage: used / parity of its last phase
     int published = 0;                        // stages published so far
-    int k = blockIdx.x;
-    while (k < n_chunks && ok) {
-      int next = 0;
-      if (lane == 0) next = G + atomicAdd(p.chunk_counter, 1);
-      const int b0 = k * C, b1 = min(total, b0 + C);
-      const bool last_chunk = k == n_chunks - 1;
-      for (int s = first_seq_at(sm.prefix, p.num_seqs, b0); s < p.num_seqs && ok; ++s) {
-        const int B = sm.prefix[s];
-        if (B >= b1 && !last_chunk) break;
-        const int nb = sm.prefix[s + 1] - B;
-        if (nb == 0) {
-          // empty context: the chunk holding its start owns it; output zero
-          uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<size_t>(s) * kHq * kD);
-          for (int e = lane; e < kHq * kD * 2 / 16; e += 32) o[e] = make_uint4(0, 0, 0, 0);
-          if (lane == 0) p.meta[s] = make_int2(0, 0);
-          continue;
+    for (int t = b0; t < b1 && ok; t += 32) {
+      const int cnt = min(32, b1 - t);
+      const TileWork cur = w;
+      if (t + 32 < b1) w = tile_work<BT>(p, sm, t + 32, b0, b1, lane);
+      for (int e = 0; e < cnt; ++e) {
+        int good = 1;
+        if (lane == e) {
+          if (!mbar_wait(&sm.empty[stage], phase ^ 1, p.wait_ns)) {
+            good = 0;
+          } else {
+            const bool valid = cur.blk >= 0 && cur.blk < p.num_blocks;
+            const bool valid2 = BT == 8 && cur.blk2 >= 0 && cur.blk2 < p.num_blocks;
+            if (!valid || (BT == 8 && cur.blk2 != -2 && !valid2)) report(p.err, PA_DEV_BAD_BLOCK);
+            StageDesc d = cur.d;
+            d.use = ((1u << cur.n_tok) - 1u) &
+                    (BT == 8 ? (valid ? 0x00ffu : 0u) | (valid2 ? 0xff00u : 0u) : (valid ? 0xffffu : 0u));
+            sm.desc[stage] = d;
+            constexpr int kPageCopy = BT == 8 ? kTileBytes / 2 : kTileBytes;
+            const int copies = (valid ? 1 : 0) + (valid2 ? 1 : 0);
+            const bool first = d.flags & kSegStart;
+            mbar_arrive_expect_tx(&sm.full[stage], copies * (kPageCopy + 2 * kHkv * 4) +
+                                                       (first ? kHq * kD * 2 : 0));
+            // test hook: this stage's copies are left out, so its barrier
+            // never completes and every wait on it runs out
+            const bool fault = p.fault_stage == published && blockIdx.x == 0;
+            if (first && !fault)
+              bulk_g2s(sm.q[stage], p.q + static_cast<size_t>(d.seq) * kHq * kD, kHq * kD * 2,
+                       &sm.full[stage]);
+            if (valid && !fault) {
+              tma_load_5d(sm.kv[stage], &kv_map, 0, BT == 32 ? (cur.j & 1) * kTile : 0, 0, 0,
+                          cur.blk, &sm.full[stage]);
+              bulk_g2s(sm.scale[stage][0], p.scales + static_cast<size_t>(cur.blk) * 2 * kHkv,
+                       2 * kHkv * 4, &sm.full[stage]);
+            }
+            if (valid2 && !fault) {
+              tma_load_5d(sm.kv[stage] + kPageCopy, &kv_map, 0, 0, 0, 0, cur.blk2, &sm.full[stage]);
+              bulk_g2s(sm.scale[stage][1], p.scales + static_cast<size_t>(cur.blk2) * 2 * kHkv,
+                       2 * kHkv * 4, &sm.full[stage]);
+            }
+          }
         }
-        if (B >= b1) break;   // last chunk: only empty sequences may follow
-        const int tail = clamped_ctx(p, s) - (nb - 1) * kTile;
-        const int jb = max(b0, B) - B, je = min(b1, B + nb) - B;
-        const int k_first = B / C;
-        const int n_parts = (B + nb - 1) / C - k_first + 1;
-        if (k == k_first && lane == 0) p.meta[s] = make_int2(k_first + s, n_parts);
-        const int32_t *row =
-            p.block_table + (static_cast<size_t>(s) * p.n_layers + p.layer) * p.max_blocks;
-        for (int j0 = jb; j0 < je && ok; j0 += 32) {
-          const int cnt = min(32, je - j0);
-          // lane i: the page of tile j0 + i (two pages for 8-token pages; the
-          // second exists when the tile has more than 8 tokens)
-          int my_blk = -1, my_blk2 = -1;
-          const int mj = j0 + lane;
-          if (lane < cnt) {
-            my_blk = row[BT == 32 ? mj >> 1 : BT == 8 ? 2 * mj : mj];
-            if (BT == 8 && (mj < nb - 1 || tail > 8)) my_blk2 = row[2 * mj + 1];
-          }
-          for (int e = 0; e < cnt; ++e) {
-            const int blk = __shfl_sync(0xffffffffu, my_blk, e);
-            const int blk2 = BT == 8 ? __shfl_sync(0xffffffffu, my_blk2, e) : -1;
-            const int j = j0 + e;
-            int good = 1;
-            if (lane == 0) good = mbar_wait(&sm.empty[stage], phase ^ 1, p.wait_ns) ? 1 : 0;
-            good = __shfl_sync(0xffffffffu, good, 0);
-            if (!good) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              const int n_tok = j == nb - 1 ? tail : kTile;
-              const bool valid = blk >= 0 && blk < p.num_blocks;
-              const bool has2 = BT == 8 && n_tok > 8;
-              const bool valid2 = has2 && blk2 >= 0 && blk2 < p.num_blocks;
-              if (!valid || (has2 && !valid2)) report(p.err, PA_DEV_BAD_BLOCK);
-              StageDesc d;
-              d.seq = s;
-              d.flags = (j == jb ? kSegStart : 0) | (j == je - 1 ? kSegEnd : 0);
-              d.slot = n_parts > 1 ? k + s : -1;
-              d.use = ((1u << n_tok) - 1u) & (BT == 8 ? (valid ? 0x00ffu : 0u) | (valid2 ? 0xff00u : 0u)
-                                                      : (valid ? 0xffffu : 0u));
-              sm.desc[stage] = d;
-              constexpr int kPageCopy = BT == 8 ? kTileBytes / 2 : kTileBytes;
-              const int copies = (valid ? 1 : 0) + (valid2 ? 1 : 0);
-              mbar_arrive_expect_tx(&sm.full[stage], copies * (kPageCopy + 2 * kHkv * 4));
-              // test hook: this stage's copies are left out, so its barrier
-              // never completes and every wait on it runs out
-              const bool fault = p.fault_stage == published && blockIdx.x == 0;
-              if (valid && !fault) {
-                tma_load_5d(sm.kv[stage], &kv_map, 0, BT == 32 ? (j & 1) * kTile : 0, 0, 0, blk,
-                            &sm.full[stage]);
-                bulk_g2s(sm.scale[stage][0], p.scales + static_cast<size_t>(blk) * 2 * kHkv,
-                         2 * kHkv * 4, &sm.full[stage]);
-              }
-              if (valid2 && !fault) {
-                tma_load_5d(sm.kv[stage] + kPageCopy, &kv_map, 0, 0, 0, 0, blk2, &sm.full[stage]);
-                bulk_g2s(sm.scale[stage][1], p.scales + static_cast<size_t>(blk2) * 2 * kHkv,
-                         2 * kHkv * 4, &sm.full[stage]);
-              }
-              issued |= 1u << stage;
-              issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-            }
-            __syncwarp();
-            ++published;
-            if (++stage == kStages) {
-              stage = 0;
-              phase ^= 1;
-            }
-          }
+        ok = __shfl_sync(0xffffffffu, good, e) != 0;
+        if (!ok) break;
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        ++published;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      k = __shfl_sync(0xffffffffu, next, 0);
-      if (k < G) k = n_chunks;   // a counter that was never zeroed
     }
     if (lane == 0) {
       if (ok && mbar_wait(&sm.empty[stage], phase ^ 1, p.wait_ns)) {
@@ -535,8 +610,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const StageDesc d = sm.desc[stage];
       if (d.flags & kEndOfWork) break;
       if (d.flags & kSegStart) {
-        const float mine = load_q(p.q + static_cast<size_t>(d.seq) * kHq * kD, warp * kGqa, g, c,
-                                  p.qscale, qa);
+        const float mine = load_q(smem_u32(sm.q[stage]) + warp * kGqa * kD * 2, g, c, p.qscale, qa);
         qs.x = __shfl_sync(0xffffffffu, mine, 8 * c);       // heads 2c, 2c + 1
         qs.y = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
         st.reset();
@@ -604,88 +678,108 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-// Combines the partials of every sequence cut into several pieces, and
-// returns the chunk counter to zero for the next call.  Grid (num_seqs, 32 q
-// heads), kShares warps = interleaved shares of the partials, lane = 2 dims.
-template <int kShares>
-__global__ void __launch_bounds__(kShares * 32) decode_q8_merge_kernel(Q8DecodeParams p) {
+// Combines the partials of every sequence cut into several pieces.  Grid
+// (num_seqs, 32 / kHeads): a CTA takes kHeads q heads, kShares warps a head, each half warp
+// every (2 kShares)-th partial, 4 dims a lane.  The cut follows from the context
+// lengths, which are read before the first kernel has ended (it waited for
+// everything before it), so that one round of loads is left after it.
+template <int kHeads, int kShares>
+__global__ void __launch_bounds__(kHeads * kShares * 32)
+    decode_q8_merge_kernel(Q8DecodeParams p, int G) {
   pdl_launch_dependents();   // the next kernel may start its own set-up
+  constexpr int kMergeThreads = kHeads * kShares * 32;
+  __shared__ int sm_sum[2];
+  __shared__ float2 sm_ml[kHeads][kShares];
+  __shared__ float4 sm_o[kHeads][kShares][kD / 4];
+  const int s = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 2) sm_sum[tid] = 0;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int i = tid; i < p.num_seqs; i += kMergeThreads) {
+    const int nb = tiles_in(clamp_ctx(p, ctx_now(p, i)));
+    all += nb;
+    if (i < s) before += nb;
+  }
+  const int mine = tiles_in(clamp_ctx(p, ctx_now(p, s)));
+  if ((tid & ~31) < p.num_seqs) {
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (lane == 0) {
+      atomicAdd(&sm_sum[0], before);
+      atomicAdd(&sm_sum[1], all);
+    }
+  }
+  __syncthreads();
+  const int B = sm_sum[0], E = B + mine;
+  const int C = max((sm_sum[1] + G - 1) / G, 1);
+  const int k0 = B / C, np = mine > 0 ? (E - 1) / C - k0 + 1 : 0;   // the runs it lies in
+  // (one CTA always waits, so that this grid ends after the first kernel)
+  if (np <= 1 && (blockIdx.x != 0 || blockIdx.y != 0)) return;
   pdl_wait_primary();
-  __shared__ float sm_m[kShares], sm_l[kShares];
-  __shared__ float2 sm_o[kShares][32];
-  const int s = blockIdx.x, h = blockIdx.y;
-  const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
-  if (s == 0 && h == 0 && threadIdx.x == 0) *p.chunk_counter = 0;   // the first kernel is done
-  const int2 mt = p.meta[s];
-  const int np = mt.y;
   if (np <= 1) return;
-  // meta left by another call may name slots beyond this workspace
-  if (mt.x < 0 || static_cast<long long>(mt.x) + np > p.n_slots) return;
-  const size_t slot0 = static_cast<size_t>(mt.x);
-  const float2 *acc = reinterpret_cast<const float2 *>(p.acc);
+  const int h = warp % kHeads, share = warp / kHeads, half = lane >> 4, d4 = lane & 15;
+  const size_t row = static_cast<size_t>(blockIdx.y) * kHeads + h;
   float m = neg_inf(), l = 0.f;
-  float2 o = make_float2(0.f, 0.f);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto fold = [&](float m2, float l2, float4 o2) {
+    const float mn = fmaxf(m, m2);
+    const float ref = mn == neg_inf() ? 0.f : mn;
+    const float so = fast_exp2(m - ref), sn = fast_exp2(m2 - ref);
+    l = fmaf(l, so, l2 * sn);
+    o = make_float4(fmaf(o.x, so, o2.x * sn), fmaf(o.y, so, o2.y * sn), fmaf(o.z, so, o2.z * sn),
+                    fmaf(o.w, so, o2.w * sn));
+    m = mn;
+  };
   // loads are issued kBatch partials at a time before any of them is folded
-  constexpr int kBatch = 8;
-  for (int k0 = share; k0 < np; k0 += kShares * kBatch) {
-    float2 mk[kBatch], a[kBatch];
+  constexpr int kBatch = 6;
+  for (int i0 = 2 * share + half; i0 < np; i0 += 2 * kShares * kBatch) {
+    float2 mk[kBatch];
+    float4 a[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int k = k0 + b * kShares;
+      const int i = i0 + b * 2 * kShares;
       mk[b] = make_float2(neg_inf(), 0.f);
-      a[b] = make_float2(0.f, 0.f);
-      if (k < np) {
-        mk[b] = p.ml[(slot0 + k) * kHq + h];
-        a[b] = acc[((slot0 + k) * kHq + h) * (kD / 2) + lane];
+      a[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < np) {
+        const size_t at = static_cast<size_t>(k0 + s + i) * kHq + row;
+        mk[b] = p.ml[at];
+        a[b] = reinterpret_cast<const float4 *>(p.acc + at * kD)[d4];
       }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (mk[b].x == neg_inf() && mk[b].y == 0.f) continue;
-      const float mn = fmaxf(m, mk[b].x);
-      const float ref = mn == neg_inf() ? 0.f : mn;
-      const float so = fast_exp2(m - ref), sn = fast_exp2(mk[b].x - ref);
-      l = fmaf(l, so, mk[b].y * sn);
-      o.x = fmaf(o.x, so, a[b].x * sn);
-      o.y = fmaf(o.y, so, a[b].y * sn);
-      m = mn;
-    }
+    for (int b = 0; b < kBatch; ++b) fold(mk[b].x, mk[b].y, a[b]);
   }
-  if (lane == 0) {
-    sm_m[share] = m;
-    sm_l[share] = l;
+  // the two halves of the warp, then the shares
+  __syncwarp();
+  auto other = [](float x) { return __shfl_xor_sync(0xffffffffu, x, 16); };
+  {
+    const float m2 = other(m), l2 = other(l);
+    const float4 o2 = make_float4(other(o.x), other(o.y), other(o.z), other(o.w));
+    fold(m2, l2, o2);
   }
-  sm_o[share][lane] = o;
-  __syncthreads();
-  if (share == 0) {
-    float M = neg_inf();
+  if (kShares > 1) {
+    if (lane == 0) sm_ml[h][share] = make_float2(m, l);
+    if (half == 0) sm_o[h][share][d4] = o;
+    __syncthreads();
+    if (share != 0) return;
 #pragma unroll
-    for (int w = 0; w < kShares; ++w) M = fmaxf(M, sm_m[w]);
-    const float ref = M == neg_inf() ? 0.f : M;
-    float L = 0.f;
-    float2 t = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kShares; ++w) {
-      const float sc = fast_exp2(sm_m[w] - ref);   // empty shares carry m = -inf: weight 0
-      L = fmaf(sm_l[w], sc, L);
-      t.x = fmaf(sm_o[w][lane].x, sc, t.x);
-      t.y = fmaf(sm_o[w][lane].y, sc, t.y);
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (static_cast<size_t>(s) * kHq + h) * kD);
-    dst[lane] = float2_to_bf16x2(t.x * inv, t.y * inv);
+    for (int w = 1; w < kShares; ++w) fold(sm_ml[h][w].x, sm_ml[h][w].y, sm_o[h][w][d4]);
+  }
+  if (half == 0) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    reinterpret_cast<uint2 *>(p.out + (static_cast<size_t>(s) * kHq + row) * kD)[d4] =
+        make_uint2(float2_to_bf16x2(o.x * inv, o.y * inv), float2_to_bf16x2(o.z * inv, o.w * inv));
   }
 }
 
 struct WsLayout {
-  size_t meta_off, ml_off, acc_off, total;
+  size_t acc_off, total;
 };
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-long long slots_for(int num_seqs, int grid) {
-  return static_cast<long long>(kChunksPerCta) * grid + 2 + num_seqs;
-}
+long long slots_for(int num_seqs, int grid) { return static_cast<long long>(grid) + num_seqs; }
 
 // Tensor map over the pool: dims (two heads' d 128, token bt, head pair 4, K|V
 // 2, block), the token dimension before the pairs although its stride is the
@@ -715,11 +809,9 @@ int make_q8_tile_map(CUtensorMap *map, const void *kv_cache, int num_blocks, int
   return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
 }
 
-WsLayout ws_layout(int num_seqs, long long slots) {
+WsLayout ws_layout(long long slots) {
   WsLayout w;
-  w.meta_off = 256;   // the chunk counter lies before it
-  w.ml_off = w.meta_off + align256(sizeof(int2) * static_cast<size_t>(num_seqs));
-  w.acc_off = w.ml_off + align256(sizeof(float2) * kHq * static_cast<size_t>(slots));
+  w.acc_off = align256(sizeof(float2) * kHq * static_cast<size_t>(slots));
   w.total = w.acc_off + align256(sizeof(float) * kHq * kD * static_cast<size_t>(slots));
   return w;
 }
@@ -761,11 +853,13 @@ int decode_q8_impl(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,
   if (rc != PA_OK) return rc;
   const int G = grid_for(di, num_seqs, tiles);
   const long long slots = slots_for(num_seqs, G);
-  const WsLayout w = ws_layout(num_seqs, slots);
+  const WsLayout w = ws_layout(slots);
   if (w.total > workspace_bytes) return PA_ERR_WORKSPACE;
-  const size_t smem = sizeof(Smem) + 1024;   // + room to align the base to 1 KiB
+  // + room to align the base to 1 KiB
+  const size_t smem = sizeof(Smem) + sizeof(int) * static_cast<size_t>(num_seqs) + 1024;
   if (cudaFuncSetAttribute(decode_q8_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+                           static_cast<int>(sizeof(Smem) + sizeof(int) * kMaxSeqs + 1024)) !=
+      cudaSuccess)
     return PA_ERR_CUDA;
   alignas(64) CUtensorMap map;
   rc = make_q8_tile_map(&map, kv_cache, num_blocks, BT);
@@ -779,9 +873,7 @@ int decode_q8_impl(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,
   prm.scales = kv_scales;
   prm.block_table = block_table;
   prm.context_lens = context_lens;
-  prm.chunk_counter = reinterpret_cast<int *>(ws);
-  prm.meta = reinterpret_cast<int2 *>(ws + w.meta_off);
-  prm.ml = reinterpret_cast<float2 *>(ws + w.ml_off);
+  prm.ml = reinterpret_cast<float2 *>(ws);
   prm.acc = reinterpret_cast<float *>(ws + w.acc_off);
   prm.err = err;
   prm.num_blocks = num_blocks;
@@ -791,15 +883,23 @@ int decode_q8_impl(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,
   prm.layer = layer;
   prm.cap_tokens = max_blocks_per_seq * BT;
   prm.qscale = scale * kLog2e;
-  prm.n_slots = slots;
   decode_fault(&prm.fault_stage, &prm.wait_ns);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prm.direct = tiles <= kDirectTiles ? 1 : 0;
+  if (prm.direct)
+    return launch_pdl(decode_q8_kernel<BT>, dim3(num_seqs), dim3(kThreads), smem, st, map, prm) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
   if (launch_pdl(decode_q8_kernel<BT>, dim3(G), dim3(kThreads), smem, st, map, prm) != cudaSuccess)
     return PA_ERR_CUDA;
+  // few sequences have many partials each
   const cudaError_t e =
-      num_seqs >= 8
-          ? launch_pdl(decode_q8_merge_kernel<4>, dim3(num_seqs, kHq), dim3(4 * 32), 0, st, prm)
-          : launch_pdl(decode_q8_merge_kernel<16>, dim3(num_seqs, kHq), dim3(16 * 32), 0, st, prm);
+      num_seqs >= 64
+          ? launch_pdl(decode_q8_merge_kernel<16, 2>, dim3(num_seqs, 2), dim3(1024), 0, st, prm, G)
+      : num_seqs >= 8
+          ? launch_pdl(decode_q8_merge_kernel<4, 4>, dim3(num_seqs, 8), dim3(512), 0, st, prm, G)
+          : launch_pdl(decode_q8_merge_kernel<1, 16>, dim3(num_seqs, 32), dim3(512), 0, st, prm, G);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -816,7 +916,7 @@ extern "C" size_t pa_decode_workspace_size_q8(int num_seqs, int max_blocks_per_s
   DeviceInfo di;
   if (current_device(&di) != PA_OK) di.sm_count = kMaxGrid;   // generous when no device answers
   const int G = grid_for(di, num_seqs, tiles_of(max_blocks_per_seq, block_tokens));
-  return ws_layout(num_seqs, slots_for(num_seqs, G)).total;
+  return ws_layout(slots_for(num_seqs, G)).total;
 }
 
 extern "C" int pa_decode_attention_q8(uint16_t *out, const uint16_t *q, const uint8_t *kv_cache,
