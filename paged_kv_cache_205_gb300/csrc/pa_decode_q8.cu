@@ -42,13 +42,14 @@
 //   Row n of a group of 8 stands for token n / 2 + 4 (n % 2): with two heads'
 //   64 bytes in a 128-byte row, swizzled by the token, the loads of both
 //   products are then free of bank conflicts.
-// The running maximum is a reference that moves only when a score exceeds it
-// by more than 2^8 (one vote a tile instead of a reduction over the tokens and
-// a rescale of O), so P <= 2^8.
+// The running maximum is a reference set 2^7 below the largest score that moves
+// only when a score exceeds it by more than 2^15 (one vote a tile instead of a
+// reduction over the tokens and a rescale of O), so P <= 2^15.
 // e4m3 becomes f16 exactly; q is scaled by a power of two per head to f16
 // (exact for values down to 2^-29 of the head's largest).  P enters the MMA in
-// f16: half a step is 2^-12 of a weight (2^-25 absolute below 2^-14), an
-// eighth of the output's own bf16 rounding; m and l stay fp32.  K's scale
+// f16: half a step is 2^-12 of a weight (2^-25 absolute below 2^-14, which is
+// 2^-32 of the largest weight), an eighth of the output's own bf16 rounding; m
+// and l stay fp32.  K's scale
 // multiplies the scores; V's multiplies the tile's product when it is added
 // to the running output.
 #include <climits>
@@ -75,7 +76,8 @@ constexpr int kPrefetchTiles = 4;          // tiles brought into L2 before the w
 constexpr int kTileBytes = 2 * kTile * kQ8TokBytes;   // K and V of 8 heads: 16 KiB
 constexpr int kPairBytes = 2 * kQ8HeadBytes;          // one token, two heads: a row of the copies
 constexpr float kNoScore = -1e30f;       // the reference before a score is seen
-constexpr float kMove = 8.f;             // log2 units a score may lie above the reference
+constexpr float kBelow = 7.f;            // log2 units the reference is set below the largest score
+constexpr float kMove = 15.f;            // and a score may lie above it
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int kSegStart = 1;   // first tile of a sequence's piece in the run
@@ -289,8 +291,8 @@ __device__ __forceinline__ void attend(uint32_t k0, uint32_t k1, uint32_t v0, ui
       nx = fmaxf(nx, __shfl_xor_sync(0xffffffffu, nx, d));
       ny = fmaxf(ny, __shfl_xor_sync(0xffffffffu, ny, d));
     }
-    nx = fmaxf(nx, st.m.x);
-    ny = fmaxf(ny, st.m.y);
+    nx = fmaxf(nx - kBelow, st.m.x);
+    ny = fmaxf(ny - kBelow, st.m.y);
     const float2 al = make_float2(fast_exp2(st.m.x - nx), fast_exp2(st.m.y - ny));
     st.m = make_float2(nx, ny);
     st.l = mul2(st.l, al);

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefill_attention_kernel(
 
   constexpr int kPagesPerChunk = PageGeom<BT>::kPages;
   constexpr unsigned kAllPages = PageGeom<BT>::kAll;
-  const int total_tiles = order_tiles<BT, kPThreads>(sm, p, tid, warp, lane);
+  const int total_tiles = order_tiles<BT, kPThreads, kSortTiles>(sm, p, tid, warp, lane);
   const int n_items = total_tiles * kHkv;
   if (static_cast<int>(blockIdx.x) >= n_items) return;
   const bool sorted = total_tiles <= kSortTiles;

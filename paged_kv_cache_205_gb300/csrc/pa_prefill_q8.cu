@@ -8,9 +8,27 @@
 // heads, 128-key chunks, S and O in TMEM, one MMA warp and one softmax
 // warpgroup a half) with a converter warpgroup between the copies and the
 // MMAs: the TMA brings a chunk's bytes (16 KiB, half of the bf16 cache's) into
-// a small ring, and four warps widen them into the operand tiles.  An e4m3
-// value times a power of two is exact in bf16, so the MMAs compute with what
-// the cache holds.
+// a small ring, and four warps widen them into f16 operand tiles, one
+// conversion for two values.  (Widened to bf16 with the scales multiplied in,
+// six instructions for two values, 8 x 2048 tokens took 259 us and 32 x 512
+// after 4096 860 us.)  The pages' scales come in in two steps.  Within a chunk a
+// page's values are multiplied by its scale over the chunk's largest, a power
+// of two; what is left is one scale a chunk for K (sK) and one for V (sV), and
+// the softmax is
+//   y = s * (f sK) + log2 sV - M     (one FMA, as for the bf16 cache)
+//   P = 2^y,  O = sum P V16,  l = sum P / sV
+// with f the item's score factor and M a reference 2^7 below the row's largest
+// s f sK + log2 sV, which moves when a chunk exceeds it by more than 2^15: M
+// follows the weights times the values' scale, so that P fits f16 (<= 2^15)
+// however far the scales lie apart.  f16 rounds a P by half a step, 2^-12 of it or
+// 2^-25 absolute below 2^-14, which is 2^-32 of the row's largest P.  A chunk
+// whose V scales lie further than 2^7 apart keeps V's bytes as they are and takes
+// log2 sV page by page, so that a heavy key in a page of small scale does not lift
+// the reference by the others' scale.  (K's scales may lie any distance apart: f16
+// takes a factor down to 2^-15 without rounding, and what is lost below weighs
+// 2^-33 of the largest key's score.)  The converter also turns an item's q
+// into f16, scaled by a power of two (f undoes it), exact for values down to
+// 2^-29 of the item's largest.
 #include "pa_prefill_shared.cuh"
 #include "pa_q8.cuh"
 #include <cuda_fp16.h>
@@ -18,32 +36,58 @@
 namespace pa {
 namespace {
 
-constexpr int kRaw = 2;                       // chunks of bytes in flight
+constexpr int kSortQ = 2048;                  // tiles ordered by weight; beyond, by index
+constexpr int kRaw = 3;                       // chunks of bytes in flight
 constexpr int kWide = 3;                      // widened chunks
 constexpr int kConvWarp = 12;                 // first of 4 converter warps
 constexpr int kConvThreads = 128;
 constexpr int kQThreads = 16 * 32;
+// A score factor's floor: a masked score (-inf) times it stays -inf, and a score
+// of at most 2^28 times it is as good as 0.
+constexpr float kTiny = 1.2e-38f;
 // Register budget: 512 threads x 128 at launch; the softmax warpgroups take
-// kQRegsSoft, the other two give up to kQRegsOther.
-constexpr int kQRegsSoft = 200;
-constexpr int kQRegsOther = 56;
-static_assert(2 * 128 * (kQRegsSoft + kQRegsOther) <= kQThreads * 128,
+// kQRegsSoft, the producer/MMA warpgroup and the converters give up to theirs.
+constexpr int kQRegsSoft = 192;
+constexpr int kQRegsMma = 80;
+constexpr int kQRegsConv = 48;
+static_assert(128 * (2 * kQRegsSoft + kQRegsMma + kQRegsConv) <= kQThreads * 128,
               "register split above the launch budget");
+
+// What the producer tells the converter about a chunk.
+struct __align__(16) RawChunk {
+  int mask;      // pages that were loaded
+  int n_live;    // keys of the chunk up to the tile's last
+  int pos;       // position of its first key
+  int flags;
+  float sk;      // the chunk's K scale
+  float lv;      // log2 of its V scale
+};
+constexpr int kFirst = 1;       // the item's first chunk: its q comes with it
+constexpr int kTwoHalves = 2;
+constexpr int kDiagonal = 4;    // some row of the tile does not see some key
+constexpr int kFarApart = 8;    // V's scales spread over more than 2^7
+constexpr int kEnd = 16;        // no more chunks
 
 struct __align__(1024) QSmem {
   unsigned char q[kQBufs][kHalves][kOperandBytes]; // per half [32 tok][4 heads][64], swizzled
-  unsigned char k[kWide][kOperandBytes];           // [128 keys][64] bf16
+  unsigned char k[kWide][kOperandBytes];           // [128 keys][64] f16
   unsigned char v[kWide][kOperandBytes];
   unsigned char raw[kRaw][2][kChunk * kQ8HeadBytes];   // [128 keys][64] e4m3, K and V
   int tile_prefix[kMaxSeqsP + 1];
   int bin_start[kWeightBins];                      // counting sort of the tiles by weight
-  uint16_t order[kSortTiles];                      // tiles, heaviest first
-  uint8_t tile_bins[kSortTiles];                   // each tile's bin
-  float2 raw_scale[kRaw][kChunk / 8];              // (sK, sV) of the chunk's pages
+  uint16_t order[kSortQ];                          // tiles, heaviest first
+  uint8_t tile_bins[kSortQ];                       // each tile's bin
+  uint2 raw_mul[kRaw][kChunk / 8];                 // per page: f16x2 factors of K's and V's bytes
+  float raw_lv[kRaw][kChunk / 8];                  // per page: log2 of V's scale
+  RawChunk raw_rec[kRaw];
+  float4 scale[kWide];                             // (f sK, log2 sV, 1 / sV, 1: V's pages far apart)
+  float lv[kWide][kChunk / 8];                     // far apart: log2 of V's scale per page
+  uint32_t q_top[4];                               // the converter warps' largest |q| (bf16 pattern)
   int nan_from[kQBufs][kD];                        // per dim: first position of the item's diagonal
                                                    // chunks whose value is NaN
   int nan_any[kQBufs];                             // some nan_from is set
   uint64_t q_full[kQBufs];
+  uint64_t q_ready[kQBufs];                        // q is f16
   uint64_t q_empty[kQBufs];
   uint64_t raw_full[kRaw];
   uint64_t raw_empty[kRaw];
@@ -57,46 +101,90 @@ struct __align__(1024) QSmem {
   uint64_t staged[kHalves];                        // the half's output rows are in shared memory
   uint64_t mma_done[kHalves];                      // every MMA of the half's warp has completed
   uint32_t tmem_base;
-  int raw_mask[kRaw];                              // pages of the chunk that were loaded
   int pmask[kWide];
   int warp_sum[kQThreads / 32];
 };
 
 static_assert(sizeof(QSmem) + 1024 <= 227 * 1024, "shared memory above the per-CTA limit");
 
-// 16 e4m3 values times `scale` as bf16.
-__device__ __forceinline__ void widen16(uint4 raw, float scale, uint4 *lo, uint4 *hi) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t h = e4m3x2_to_f16x2(w[i >> 1] >> (16 * (i & 1)));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    o[i] = float2_to_bf16x2(f.x * scale, f.y * scale);
-  }
-  *lo = make_uint4(o[0], o[1], o[2], o[3]);
-  *hi = make_uint4(o[4], o[5], o[6], o[7]);
+// Two packed e4m3 times mul (two f16).
+__device__ __forceinline__ uint32_t widen2(uint32_t pair, uint32_t mul) {
+  const uint32_t h = e4m3x2_to_f16x2(pair);
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(mul));
+  return r;
+}
+// 8 e4m3 values times mul as f16.
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t mul) {
+  return make_uint4(widen2(a, mul), widen2(a >> 16, mul), widen2(b, mul), widen2(b >> 16, mul));
 }
 
-// Whether one of 16 e4m3 bytes is NaN (0x7f or 0xff).
-__device__ __forceinline__ bool has_nan(uint4 r) {
-  const uint32_t m = 0x7f7f7f7fu, one = 0x01010101u;
-  return ((((r.x & m) + one) | ((r.y & m) + one) | ((r.z & m) + one) | ((r.w & m) + one)) &
-          0x80808080u) != 0;
+// Two f16 2^d (d <= 0; 0 below f16's smallest number).
+__device__ __forceinline__ uint32_t pow2_f16x2(int d) {
+  const uint32_t h = d >= -14 ? static_cast<uint32_t>(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
+  return h | (h << 16);
 }
 
-// The bytes with NaN replaced by zero; from[d] takes the position of a NaN in
-// dim d when it is the first.  Rare.
-__device__ __noinline__ uint4 without_nan(uint4 r, int dim0, int pos, int *from) {
-  uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  for (int i = 0; i < 16; ++i) {
-    const int sh = 8 * (i & 3);
-    if (((w[i >> 2] >> sh) & 0x7fu) == 0x7fu) {
-      w[i >> 2] &= ~(0xffu << sh);
-      atomicMin(from + dim0 + i, pos);
-    }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The largest |q| (bf16 pattern) of row r of a half's q tile (128-byte rows,
+// 16-byte chunk e at e ^ (r & 7)).
+__device__ __forceinline__ uint32_t q_row_top(const unsigned char *row, int r) {
+  uint32_t top = 0;
+#pragma unroll 2
+  for (int e = 0; e < kD / 8; ++e) {
+    const uint4 w = *reinterpret_cast<const uint4 *>(row + ((e ^ (r & 7)) << 4));
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                 __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return max(top & 0xffffu, top >> 16);
+}
+
+// The row from bf16 to f16 in place, times `up`.
+__device__ __forceinline__ void q_row_to_f16(unsigned char *row, int r, float up) {
+#pragma unroll 2
+  for (int e = 0; e < kD / 8; ++e) {
+    uint4 *at = reinterpret_cast<uint4 *>(row + ((e ^ (r & 7)) << 4));
+    const uint4 w = *at;
+    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+    const float2 c = bf16x2_to_float2(w.z), d = bf16x2_to_float2(w.w);
+    *at = make_uint4(pack_f16(a.x * up, a.y * up), pack_f16(b.x * up, b.y * up),
+                     pack_f16(c.x * up, c.y * up), pack_f16(d.x * up, d.y * up));
+  }
+}
+
+// The top bits of the bytes that are NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// w with its NaN bytes (`nan`, from nan_bytes) replaced by zeros; from[d] takes
+// the position of a NaN in dim d when it is the first.  Rare.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, int dim0, int pos, int *from) {
+  for (uint32_t m = nan_bytes(w); m; m &= m - 1) {
+    const int byte = (__ffs(m) - 1) >> 3;
+    w &= ~(0xffu << (8 * byte));
+    atomicMin(from + dim0 + byte, pos);
+  }
+  return w;
+}
+
+// Whether `mine` holds in all converter threads (a barrier among them: they take
+// the same way past a wait that ran out in some).
+__device__ __forceinline__ bool converters_agree(bool mine) {
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(mine ? 1 : 0), "n"(kConvThreads)
+      : "memory");
+  return all != 0;
 }
 
 // MMA warp: waits until chunk gc is widened (every MMA warp does, for every
@@ -150,6 +238,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
     prefetch_tensormap(&out_map);
     for (int b = 0; b < kQBufs; ++b) {
       mbar_init(&sm.q_full[b], 1);
+      mbar_init(&sm.q_ready[b], kConvThreads);
       // the MMA warps' commits and each softmax half once its output left
       // the buffer (it stages the half's output tile there)
       mbar_init(&sm.q_empty[b], 2 * kHalves);
@@ -180,10 +269,10 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
 
   constexpr int kPagesPerChunk = PageGeom<BT>::kPages;
   constexpr unsigned kAllPages = PageGeom<BT>::kAll;
-  const int total_tiles = order_tiles<BT, kQThreads>(sm, p, tid, warp, lane);
+  const int total_tiles = order_tiles<BT, kQThreads, kSortQ>(sm, p, tid, warp, lane);
   const int n_items = total_tiles * kHkv;
   if (static_cast<int>(blockIdx.x) >= n_items) return;
-  const bool sorted = total_tiles <= kSortTiles;
+  const bool sorted = total_tiles <= kSortQ;
 
   if (warp == kMmaWarp) {
     tc::tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -193,75 +282,93 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
-  if (warp >= 8) {
-    // the producer/MMA warpgroup gives registers to the softmax warpgroups
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQRegsOther));
+  if (warp >= 8 && warp < kConvWarp) {
+    // this warpgroup and the converters' give registers to the softmax warpgroups
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQRegsMma));
     if (warp == kProducerWarp) {
       // ===================================================== producer warp ==
       bool ok = true;
       int gc = 0, k = 0;
       uint32_t issued = 0, issued_parity = 0;   // per stage: used / parity of its last fill
-      // Lane l < kPagesPerChunk holds the block id of page l of a chunk and the
-      // head's scales there.  Those of the next chunk (of this item or the
-      // next) are read while this chunk's copies are issued.
-      struct Ids {
+      // Page ids and scales are read for 32 pages (kBatch chunks) at a time, a
+      // lane per page: a batch's ids when the batch before it starts, its scales
+      // once that one's first chunk is on its way.
+      constexpr int kBatch = 32 / kPagesPerChunk;
+      struct Pages {
         int blk;
         float sk, sv;
       };
-      auto chunk_ids = [&](const Item &x, int j) -> Ids {
-        Ids d;
+      auto page_ids = [&](const Item &x, int first) -> int {
         const int32_t *row =
             p.block_table + (static_cast<size_t>(x.s) * p.n_layers + p.layer) * p.max_blocks;
-        const int pg = j * kPagesPerChunk + (lane & (kPagesPerChunk - 1));
-        d.blk = (lane < kPagesPerChunk && pg * BT < x.n_keys) ? row[pg] : -1;
-        d.sk = d.sv = 0.f;
+        const int pg = first + lane;
+        return static_cast<long long>(pg) * BT < x.n_keys ? row[pg] : -1;
+      };
+      auto page_scales = [&](int g, Pages &d) {
+        d.sk = d.sv = 1.f;
         if (d.blk >= 0 && d.blk < p.num_blocks) {
-          const float *s = scales + static_cast<size_t>(d.blk) * 2 * kHkv + x.g;
+          const float *s = scales + static_cast<size_t>(d.blk) * 2 * kHkv + g;
           d.sk = s[0];
           d.sv = s[kHkv];
         }
-        return d;
       };
-      Ids next = {-1, 0.f, 0.f};
-      bool next_read = false;
-      for (; ok; ++k) {
-        const ItemRef ref = fetch_item(sm, p, total_tiles, sorted, k, n_items);
-        if (ref.i < 0) break;
+      Pages cur = {-1, 1.f, 1.f}, next = cur;
+      int next_g = 0, next_has = 0;   // of `next`: kv head; 0 nothing, 1 ids, 2 scales too
+      int q_asked = 0;    // lane 0: items whose Q has been asked for
+      // Q buffer kk % 2: the item before last has left it
+      auto ask_q = [&](const Item &x, int kk, unsigned long long wait_ns) -> bool {
+        const int qb = kk % kQBufs;
+        if (kk >= kQBufs && !mbar_wait(&sm.q_empty[qb], (kk / kQBufs - 1) & 1, wait_ns)) return false;
+        mbar_arrive_expect_tx(&sm.q_full[qb], x.halves * kOperandBytes);
+        for (int h = 0; h < x.halves; ++h)
+          tma_load_3d(sm.q[qb][h], &q_map, 0, x.g * kGqa, x.row0 + x.t0 + h * kQTok, &sm.q_full[qb]);
+        q_asked = kk + 1;
+        return true;
+      };
+      ItemRef ref = fetch_item(sm, p, total_tiles, sorted, 0, n_items);
+      for (; ok && ref.i >= 0; ++k) {
         const Item it = decode_item(sm, ref);
-        if (!next_read && it.n_chunks > 0) next = chunk_ids(it, 0);
-        next_read = false;
-        int good = 1;
-        if (lane == 0) {
-          // Q buffer k % 2: the MMAs of the item before last have read it
-          const int qb = k % kQBufs;
-          if (k >= kQBufs && !mbar_wait(&sm.q_empty[qb], (k / kQBufs - 1) & 1, p.wait_ns)) {
-            good = 0;
-          } else {
-            mbar_arrive_expect_tx(&sm.q_full[qb], it.halves * kOperandBytes);
-            for (int h = 0; h < it.halves; ++h)
-              tma_load_3d(sm.q[qb][h], &q_map, 0, it.g * kGqa, it.row0 + it.t0 + h * kQTok,
-                          &sm.q_full[qb]);
-          }
+        if (next_has == 0) {
+          next.blk = page_ids(it, 0);
+          next_g = it.g;
+          next_has = 1;
         }
+        int good = 1;
+        if (lane == 0 && q_asked <= k) good = ask_q(it, k, p.wait_ns) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, good, 0) != 0;
         // an item whose Q was not asked for is not waited for below
         if (!ok) break;
+        ref = fetch_item(sm, p, total_tiles, sorted, k + 1, n_items);
         for (int j = 0; j < it.n_chunks && ok; ++j, ++gc) {
           const int st = gc % kRaw;
           const uint32_t ph = (gc / kRaw) & 1;
-          const int pg = j * kPagesPerChunk + (lane & (kPagesPerChunk - 1));
-          const bool needed = lane < kPagesPerChunk && pg * BT < it.n_keys;
-          const Ids now = next;
-          if (j + 1 < it.n_chunks) {
-            next = chunk_ids(it, j + 1);
-          } else {
-            const ItemRef nr = fetch_item(sm, p, total_tiles, sorted, k + 1, n_items);
-            if (nr.i >= 0) {
-              const Item nx = decode_item(sm, nr);
-              if (nx.n_chunks > 0) next = chunk_ids(nx, 0);
-              next_read = true;
+          if (j % kBatch == 0) {
+            if (next_has == 1) page_scales(next_g, next);
+            cur = next;
+            next_has = 0;
+            if (j + kBatch < it.n_chunks) {
+              next.blk = page_ids(it, (j / kBatch + 1) * 32);
+              next_g = it.g;
+              next_has = 1;
+            } else if (ref.i >= 0) {
+              const Item nx = decode_item(sm, ref);
+              next.blk = page_ids(nx, 0);
+              next_g = nx.g;
+              next_has = 1;
             }
           }
+          // the next item's Q, once the item before this one has left its buffer
+          if (ref.i >= 0 && lane == 0 && q_asked <= k + 1 &&
+              (k == 0 || mbar_try_wait_short(&sm.q_empty[(k + 1) % kQBufs], ((k + 1) / kQBufs - 1) & 1)))
+            ask_q(decode_item(sm, ref), k + 1, p.wait_ns);
+          // lane l: page l mod kPagesPerChunk of the chunk
+          const int src = (j % kBatch) * kPagesPerChunk + (lane & (kPagesPerChunk - 1));
+          Pages now;
+          now.blk = __shfl_sync(0xffffffffu, cur.blk, src);
+          now.sk = __shfl_sync(0xffffffffu, cur.sk, src);
+          now.sv = __shfl_sync(0xffffffffu, cur.sv, src);
+          const int pg = j * kPagesPerChunk + (lane & (kPagesPerChunk - 1));
+          const bool needed = lane < kPagesPerChunk && pg * BT < it.n_keys;
           const bool valid = needed && now.blk >= 0 && now.blk < p.num_blocks;
           const unsigned vm = __ballot_sync(0xffffffffu, valid) & kAllPages;
           const unsigned nm = __ballot_sync(0xffffffffu, needed) & kAllPages;
@@ -272,10 +379,27 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           }
           ok = __shfl_sync(0xffffffffu, good, 0) != 0;
           if (!ok) break;
-          if (lane < kPagesPerChunk) sm.raw_scale[st][lane] = make_float2(now.sk, now.sv);
+          // the chunk's scales are its largest page's (exponent fields)
+          const int ek = __float_as_int(now.sk) >> 23, ev = __float_as_int(now.sv) >> 23;
+          const int top_k = __reduce_max_sync(0xffffffffu, valid ? ek : 1);
+          const int top_v = __reduce_max_sync(0xffffffffu, valid ? ev : 1);
+          const bool far = __reduce_min_sync(0xffffffffu, valid ? ev : top_v) < top_v - 7;
+          if (lane < kPagesPerChunk) {
+            sm.raw_mul[st][lane] = make_uint2(pow2_f16x2(valid ? ek - top_k : 0),
+                                              pow2_f16x2(valid && !far ? ev - top_v : 0));
+            sm.raw_lv[st][lane] = static_cast<float>((valid ? ev : top_v) - 127);
+          }
           __syncwarp();
           if (lane == 0) {
-            sm.raw_mask[st] = static_cast<int>(vm);
+            RawChunk c;
+            c.mask = static_cast<int>(vm);
+            c.pos = j * kChunk;
+            c.n_live = it.n_keys - c.pos;
+            c.flags = (j == 0 ? kFirst : 0) | (it.halves == 2 ? kTwoHalves : 0) |
+                      (c.pos + kChunk - 1 > it.ctx + it.t0 ? kDiagonal : 0) | (far ? kFarApart : 0);
+            c.sk = __int_as_float(top_k << 23);
+            c.lv = static_cast<float>(top_v - 127);
+            sm.raw_rec[st] = c;
             mbar_arrive_expect_tx(&sm.raw_full[st], __popc(vm) * 2 * BT * kQ8HeadBytes);
             issued |= 1u << st;
             issued_parity = (issued_parity & ~(1u << st)) | (ph << st);
@@ -284,19 +408,31 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           // lane l < 2 kPagesPerChunk: the K rows (l < kPagesPerChunk) or the
           // V rows of page l mod kPagesPerChunk
           const int pl = lane & (kPagesPerChunk - 1), kv = (lane / kPagesPerChunk) & 1;
-          const int pblk = __shfl_sync(0xffffffffu, now.blk, pl);
           // (test hook: CTA 0 leaves this chunk's copies out, so that the
           // waits on it run out)
           const bool fault = p.fault_chunk == gc && blockIdx.x == 0;
           if (!fault && lane < 2 * kPagesPerChunk && ((vm >> pl) & 1u))
-            tma_load_5d(sm.raw[st][kv] + pl * BT * kQ8HeadBytes, &kv_map, 0, it.g, 0, kv, pblk,
+            tma_load_5d(sm.raw[st][kv] + pl * BT * kQ8HeadBytes, &kv_map, 0, it.g, 0, kv, now.blk,
                         &sm.raw_full[st]);
+          if (next_has == 1) {
+            page_scales(next_g, next);
+            next_has = 2;
+          }
         }
       }
       if (lane == 0) {
-        if (!ok) report(p.err, PA_DEV_TIMEOUT);
+        const int st = gc % kRaw;
+        const uint32_t ph = (gc / kRaw) & 1;
+        if (ok && mbar_wait(&sm.raw_empty[st], ph ^ 1, p.wait_ns)) {
+          sm.raw_rec[st].flags = kEnd;
+          mbar_arrive(&sm.raw_full[st]);
+          issued |= 1u << st;
+          issued_parity = (issued_parity & ~(1u << st)) | (ph << st);
+        } else {
+          report(p.err, PA_DEV_TIMEOUT);
+        }
         // no copy may still be landing in shared memory when the CTA exits
-        for (int kk = max(0, k - kQBufs); kk < k; ++kk)
+        for (int kk = max(0, q_asked - kQBufs); kk < q_asked; ++kk)
           if (!mbar_wait(&sm.q_full[kk % kQBufs], (kk / kQBufs) & 1, p.wait_ns)) report(p.err, PA_DEV_TIMEOUT);
         for (int st = 0; st < kRaw; ++st)
           if ((issued >> st) & 1u)
@@ -307,8 +443,8 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
     } else if (warp < kMmaWarp + kHalves) {
       // ======================================================== MMA warps ==
       const int h = warp - kMmaWarp;     // the half whose MMAs this warp issues
-      const uint32_t id_s = tc::idesc_bf16(kRows, kChunk, false);
-      const uint32_t id_o = tc::idesc_bf16(kRows, kD, true);
+      const uint32_t id_s = tc::idesc_f16(kRows, kChunk, false);
+      const uint32_t id_o = tc::idesc_f16(kRows, kD, true);
       int ok = 1;
       int gc = 0, k = 0;
       int n_p = 0;             // P chunks of this half consumed
@@ -335,7 +471,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         const Item it = decode_item(sm, ref);
         qb = k % kQBufs;
         const int nch = h == 0 ? it.nc0 : it.nc1;
-        if (lane == 0) ok = mbar_wait_short(&sm.q_full[qb], (k / kQBufs) & 1, p.wait_ns) ? 1 : 0;
+        if (lane == 0) ok = mbar_wait_short(&sm.q_ready[qb], (k / kQBufs) & 1, p.wait_ns) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (ok) ok = mma_wait_chunk(sm, gc, lane, p.wait_ns);
         if (ok && nch > 0) ok = issue_s(gc) ? 1 : 0;
@@ -381,77 +517,99 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
       __syncwarp();
       if (lane == 0 && !mbar_wait(&sm.mma_done[h], 0, p.wait_ns)) report(p.err, PA_DEV_TIMEOUT);
       __syncwarp();
-    } else if (warp >= kConvWarp) {
+    }
+  } else if (warp >= kConvWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQRegsConv));
       // ================================================== converter warps ==
-      // A chunk's bytes as the TMA left them ([128 keys][64] of K and of V)
-      // become bf16 operand tiles, scaled, in the swizzled layout that the
-      // MMAs read.  V rows past the tile's last key or in a page that was not
-      // loaded become zeros: they meet P = 0.
-      bool ok = true;
-      int gc = 0;
-      const int ct = tid - kConvWarp * 32;
-      ItemRef ref = fetch_item(sm, p, total_tiles, sorted, 0, n_items);
-      for (int k = 0; ok && ref.i >= 0; ++k) {
-        const Item it = decode_item(sm, ref);
-        ref = fetch_item(sm, p, total_tiles, sorted, k + 1, n_items);
+    // A chunk's bytes as the TMA left them ([128 keys][64] of K and of V) become
+    // f16 operand tiles in the swizzled layout that the MMAs read; an item's q
+    // becomes f16 first.  V rows past the tile's last key or in a page that was
+    // not loaded become zeros: they meet P = 0.
+    bool ok = true;
+    const int ct = tid - kConvWarp * 32;
+    // this thread's 16-byte units of a chunk are u = ct + 128 i: key ct / 4 +
+    // 32 i, dims 16 (ct % 4) ..; their two 16-byte places in the wide row
+    const int key0 = ct >> 2, part = ct & 3;
+    const uint32_t at0 = key0 * kTileRowBytes + (((2 * part) ^ (key0 & 7)) << 4), at1 = at0 ^ 16;
+    int items = 0;
+    float factor = 0.f;
+    for (int gc = 0;; ++gc) {
+      const int rs = gc % kRaw, ws = gc % kWide;
+      ok = mbar_wait_short(&sm.raw_full[rs], (gc / kRaw) & 1, p.wait_ns);
+      if (!ok) break;
+      const RawChunk rec = sm.raw_rec[rs];
+      if (rec.flags & kEnd) break;
+      const int qb = (items + ((rec.flags & kFirst) ? 0 : 1)) % kQBufs;   // (items counts this one already)
+      if (rec.flags & kFirst) {
         // the item's Q is in, so the outputs of the item that had its buffer are out
-        const int qb = k % kQBufs;
-        ok = mbar_wait_short(&sm.q_full[qb], (k / kQBufs) & 1, p.wait_ns);
+        ok = converters_agree(mbar_wait_short(&sm.q_full[qb], (items / kQBufs) & 1, p.wait_ns));
+        if (!ok) break;
         if (ct < kD) sm.nan_from[qb][ct] = INT_MAX;
         if (ct == 0) sm.nan_any[qb] = 0;
+        // the item's q in f16, scaled to [2^12, 2^13)
+        const int halves = (rec.flags & kTwoHalves) ? 2 : 1;
+        uint32_t top = 0;
+        for (int h = 0; h < halves; ++h)
+          top = max(top, q_row_top(sm.q[qb][h] + ct * kTileRowBytes, ct));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) sm.q_top[warp & 3] = top;
         asm volatile("bar.sync 1, %0;" ::"n"(kConvThreads) : "memory");
-        for (int j = 0; j < it.n_chunks && ok; ++j, ++gc) {
-          // keys that some row of the tile does not see
-          const bool diagonal = j * kChunk + kChunk - 1 > it.ctx + it.t0;
-          const int rs = gc % kRaw, ws = gc % kWide;
-          if (!mbar_wait_short(&sm.raw_full[rs], (gc / kRaw) & 1, p.wait_ns) ||
-              !mbar_wait_short(&sm.kv_empty[ws], ((gc / kWide) & 1) ^ 1, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          const int pm = sm.raw_mask[rs];
-#pragma unroll
-          for (int i = 0; i < kChunk * 4 / kConvThreads; ++i) {
-            const int u = ct + i * kConvThreads;    // 16 bytes: key u / 4, dims 16 (u % 4) ..
-            const int key = u >> 2, part = u & 3;
-            const bool live = j * kChunk + key < it.n_keys && ((pm >> (key / BT)) & 1);
-            const float2 s = sm.raw_scale[rs][key / BT];
-            const uint4 kr = reinterpret_cast<const uint4 *>(sm.raw[rs][0])[u];
-            uint4 vr = reinterpret_cast<const uint4 *>(sm.raw[rs][1])[u];
-            if (!live) vr = make_uint4(0, 0, 0, 0);
-            // a NaN value would reach the rows before it too (P = 0 times NaN)
-            if (diagonal && has_nan(vr)) {
-              vr = without_nan(vr, 16 * part, j * kChunk + key, sm.nan_from[qb]);
-              sm.nan_any[qb] = 1;
-            }
-            const uint32_t row = key * kTileRowBytes;
-            const uint32_t c0 = ((2 * part) ^ (key & 7)) << 4, c1 = ((2 * part + 1) ^ (key & 7)) << 4;
-            uint4 lo, hi;
-            widen16(kr, s.x, &lo, &hi);
-            *reinterpret_cast<uint4 *>(sm.k[ws] + row + c0) = lo;
-            *reinterpret_cast<uint4 *>(sm.k[ws] + row + c1) = hi;
-            widen16(vr, live ? s.y : 0.f, &lo, &hi);
-            *reinterpret_cast<uint4 *>(sm.v[ws] + row + c0) = lo;
-            *reinterpret_cast<uint4 *>(sm.v[ws] + row + c1) = hi;
-          }
-          if (ct == 0) sm.pmask[ws] = pm;
-          mbar_arrive(&sm.raw_empty[rs]);
-          fence_proxy_async_smem();     // the tensor core reads the tiles through the async proxy
-          mbar_arrive(&sm.kv_full[ws]);
-        }
+        top = max(max(sm.q_top[0], sm.q_top[1]), max(sm.q_top[2], sm.q_top[3]));
+        const int f = min(266 - static_cast<int>(top >> 7), 253);   // exponent field of the scale
+        for (int h = 0; h < halves; ++h)
+          q_row_to_f16(sm.q[qb][h] + ct * kTileRowBytes, ct, __int_as_float(f << 23));
+        factor = p.qscale * __int_as_float((254 - f) << 23);
+        fence_proxy_async_smem();       // the tensor core reads q through the async proxy
+        mbar_arrive(&sm.q_ready[qb]);
+        ++items;
       }
-      if (!ok) report(p.err, PA_DEV_TIMEOUT);
+      ok = mbar_wait_short(&sm.kv_empty[ws], ((gc / kWide) & 1) ^ 1, p.wait_ns);
+      if (!ok) break;
+#pragma unroll 1
+      for (int i = 0; i < kChunk * 4 / kConvThreads; ++i) {
+        const int key = key0 + i * (kConvThreads / 4);
+        const uint2 mul = sm.raw_mul[rs][key / BT];
+        const uint32_t row = i * (kConvThreads / 4 * kTileRowBytes);
+        const uint4 kr = reinterpret_cast<const uint4 *>(sm.raw[rs][0])[ct + i * kConvThreads];
+        *reinterpret_cast<uint4 *>(sm.k[ws] + row + at0) = widen8(kr.x, kr.y, mul.x);
+        *reinterpret_cast<uint4 *>(sm.k[ws] + row + at1) = widen8(kr.z, kr.w, mul.x);
+        uint4 vr = reinterpret_cast<const uint4 *>(sm.raw[rs][1])[ct + i * kConvThreads];
+        if (key >= rec.n_live || !((rec.mask >> (key / BT)) & 1)) vr = make_uint4(0, 0, 0, 0);
+        // a NaN value would reach the rows before it too (P = 0 times NaN)
+        if ((rec.flags & kDiagonal) &&
+            (nan_bytes(vr.x) | nan_bytes(vr.y) | nan_bytes(vr.z) | nan_bytes(vr.w)) != 0) {
+          int *from = sm.nan_from[qb] + 16 * part;
+          vr.x = without_nan(vr.x, 0, rec.pos + key, from);
+          vr.y = without_nan(vr.y, 4, rec.pos + key, from);
+          vr.z = without_nan(vr.z, 8, rec.pos + key, from);
+          vr.w = without_nan(vr.w, 12, rec.pos + key, from);
+          sm.nan_any[qb] = 1;
+        }
+        *reinterpret_cast<uint4 *>(sm.v[ws] + row + at0) = widen8(vr.x, vr.y, mul.y);
+        *reinterpret_cast<uint4 *>(sm.v[ws] + row + at1) = widen8(vr.z, vr.w, mul.y);
+      }
+      if (ct < kPagesPerChunk) sm.lv[ws][ct] = sm.raw_lv[rs][ct];
+      if (ct == 0) {
+        sm.pmask[ws] = rec.mask;
+        sm.scale[ws] = make_float4(fmaxf(factor * rec.sk, kTiny), rec.lv, p_exp2(-rec.lv),
+                                   (rec.flags & kFarApart) ? 1.f : 0.f);
+      }
+      mbar_arrive(&sm.raw_empty[rs]);
+      fence_proxy_async_smem();         // the tensor core reads the tiles through the async proxy
+      mbar_arrive(&sm.kv_full[ws]);
     }
+    if (!ok) report(p.err, PA_DEV_TIMEOUT);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQRegsSoft));
     // ==================================================== softmax warps ==
-    // O accumulates in TMEM.  Each row keeps the reference maximum m its
-    // P values are taken against; it moves (and O, l are rescaled) only
-    // when a chunk's maximum exceeds it by more than kRescale (log2 units),
-    // so P stays below 2^kRescale and most chunks touch O not at all.
+    // O accumulates in TMEM.  Each row keeps the reference m its P values are
+    // taken against: kBelow (log2 units) below the largest so far when it is
+    // set; it moves (and O, l are rescaled) only when a chunk's maximum exceeds
+    // it by more than kRescale, so P stays below 2^kRescale and most chunks touch
+    // O not at all.
     // S_{j+1} is issued before PV_j, so O (for a rescale) and the P
     // columns are touched only once PV_{j-1}'s commit is there.
-    constexpr float kRescale = 8.f;
+    constexpr float kBelow = 7.f, kRescale = 15.f;
     const int h = tid >> 7;                   // half
     const int r = tid & (kRows - 1);          // MMA row = TMEM lane
     const int tok = r >> 2, hh = r & 3;
@@ -510,85 +668,137 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         // every key of the chunk is visible to every row of the half and was loaded
         const bool full = pm == static_cast<int>(kAllPages) && kbase + kChunk - 1 <= first_pos;
         const int lim = qpos - kbase;           // keys c <= lim are at or before the row
-        uint32_t v[kChunk];
-#pragma unroll
-        for (int c0 = 0; c0 < kChunk; c0 += 32)
-          tc::tmem_ld32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
-        tc::tmem_ld_wait();
-        tc::fence_before_sync();
-        mbar_arrive(&sm.s_free[h]);             // S_{j+1} may land in the S columns
-        if (!full) {
-          // masked keys: -inf (loaded K rows past the tile or in a missing page may be anything)
-#pragma unroll
-          for (int c = 0; c < kChunk; ++c)
-            if (!((c <= lim) && ((pm >> (c / BT)) & 1))) v[c] = 0xff800000u;
-        }
-        // row maximum: 8 chains of three-input maxima over keys q, q+8, ..
-        float mx8[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) mx8[q] = p_neg_inf();
-#pragma unroll
-        for (int c = 0; c < kChunk; c += 16)
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            mx8[q] = fmax3(mx8[q], __uint_as_float(v[c + q]), __uint_as_float(v[c + 8 + q]));
-        const float mc = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * p.qscale;
-        const bool move = mc > m + kRescale || (m == p_neg_inf() && mc != p_neg_inf());
+        const float4 sc = sm.scale[st];         // f sK, log2 sV, 1 / sV, V's pages far apart
+        const float2 f2 = make_float2(sc.x, sc.x);
         bool pv_done = j == 0;                  // PV_{j-1} complete: O stable, P columns read
-        if (__any_sync(0xffffffffu, move) && j > 0) {
-          if (!mbar_wait_short(&sm.o_full[h], n_o & 1, p.wait_ns)) {
-            ok = false;
-            break;
-          }
+        auto wait_pv = [&]() -> bool {
+          if (pv_done) return true;
+          if (!mbar_wait_short(&sm.o_full[h], n_o & 1, p.wait_ns)) return false;
           ++n_o;
           pv_done = true;
           tc::fence_after_sync();
-          // rescale O (the whole warp takes part in the TMEM round trip)
-          const float alpha = move ? p_exp2(m - mc) : 1.f;
+          return true;
+        };
+        // The reference moves to the chunk's maximum mc where that lies far
+        // above it; O and l follow.
+        auto move_to = [&](float mc) -> bool {
+          const bool move = mc > m + kRescale || (m == p_neg_inf() && mc != p_neg_inf());
+          if (__any_sync(0xffffffffu, move) && j > 0) {
+            if (!wait_pv()) return false;
+            // (the whole warp takes part in the TMEM round trip)
+            const float alpha = move ? p_exp2(m - (mc - kBelow)) : 1.f;
 #pragma unroll 1
-          for (int c0 = 0; c0 < kD; c0 += 32) {
-            uint32_t ov[32];
-            tc::tmem_ld32(o_addr + c0, ov);
-            tc::tmem_ld_wait();
+            for (int c0 = 0; c0 < kD; c0 += 32) {
+              uint32_t ov[32];
+              tc::tmem_ld32(o_addr + c0, ov);
+              tc::tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
-            tc::tmem_st32(o_addr + c0, ov);
+              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+              tc::tmem_st32(o_addr + c0, ov);
+            }
+            tc::tmem_st_wait();
+            l *= alpha;
           }
-          tc::tmem_st_wait();
-          l *= alpha;
-        }
-        if (move) m = mc;
-        const float base = (m == p_neg_inf()) ? 0.f : m;
-        const float2 qs2 = make_float2(p.qscale, p.qscale), nb2 = make_float2(-base, -base);
-        // P = exp2(s * qscale - m) in bf16 pairs (key 2c in the low half of
-        // column c) into the half's P columns of tensor memory; 4 partial sums
-        float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                        make_float2(0.f, 0.f)};
-        uint32_t pw[kChunk / 2];
+          if (move) m = mc - kBelow;
+          return true;
+        };
+        // P = 2^(s f sK + log2 sV - m) in f16 pairs (key 2c in the low half of
+        // column c) goes into the half's P columns of tensor memory.
+        if (sc.w == 0.f) {
+          uint32_t v[kChunk];
 #pragma unroll
-        for (int ch = 0; ch < kChunk / 8; ++ch) {
+          for (int c0 = 0; c0 < kChunk; c0 += 32)
+            tc::tmem_ld32(s_addr + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[c0]));
+          tc::tmem_ld_wait();
+          tc::fence_before_sync();
+          mbar_arrive(&sm.s_free[h]);           // S_{j+1} may land in the S columns
+          if (!full) {
+            // masked keys: -inf (loaded K rows past the tile or in a missing page may be anything)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = 8 * ch + 2 * q;
-            const float2 x = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                                  qs2, nb2);
-            const float e0 = p_exp2(x.x), e1 = p_exp2(x.y);
-            ls[q] = add2(ls[q], make_float2(e0, e1));
-            pw[c >> 1] = float2_to_bf16x2(e0, e1);
+            for (int c = 0; c < kChunk; ++c)
+              if (!((c <= lim) && ((pm >> (c / BT)) & 1))) v[c] = 0xff800000u;
           }
-        }
-        if (!pv_done) {
-          if (!mbar_wait_short(&sm.o_full[h], n_o & 1, p.wait_ns)) {
+          // row maximum: 8 chains of three-input maxima over keys q, q+8, ..
+          float mx8[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) mx8[q] = p_neg_inf();
+#pragma unroll
+          for (int c = 0; c < kChunk; c += 16)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              mx8[q] = fmax3(mx8[q], __uint_as_float(v[c + q]), __uint_as_float(v[c + 8 + q]));
+          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          if (!move_to(fmaf(mx, sc.x, sc.y))) {
             ok = false;
             break;
           }
-          ++n_o;
-          tc::fence_after_sync();
+          const float bias = sc.y - ((m == p_neg_inf()) ? 0.f : m);
+          const float2 b2 = make_float2(bias, bias);
+          float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                          make_float2(0.f, 0.f)};
+          uint32_t pw[kChunk / 2];
+#pragma unroll
+          for (int c = 0; c < kChunk; c += 2) {
+            const float2 x =
+                fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), f2, b2);
+            const float2 e = make_float2(p_exp2(x.x), p_exp2(x.y));
+            ls[(c >> 1) & 3] = add2(ls[(c >> 1) & 3], e);
+            pw[c >> 1] = pack_f16(e.x, e.y);
+          }
+          if (!wait_pv()) {
+            ok = false;
+            break;
+          }
+          tc::tmem_st32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&pw[0]));
+          tc::tmem_st32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[32]));
+          l = fmaf(((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) +
+                       ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y)), sc.z, l);
+        } else {
+          // pages far apart: log2 sV page by page, S read twice, 8 keys at a
+          // time (rare, so kept small)
+          auto load8 = [&](int c0, float (&x)[8]) {
+            uint32_t u[8];
+            tc::tmem_ld8(s_addr + c0, u);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              x[c] = (c0 + c <= lim && ((pm >> (c0 / BT)) & 1)) ? __uint_as_float(u[c]) : p_neg_inf();
+          };
+          float mc = p_neg_inf();
+#pragma unroll 1
+          for (int c0 = 0; c0 < kChunk; c0 += 8) {
+            float x[8];
+            load8(c0, x);
+            float mx = x[0];
+#pragma unroll
+            for (int c = 1; c < 8; ++c) mx = fmaxf(mx, x[c]);
+            mc = fmaxf(mc, fmaf(mx, sc.x, sm.lv[st][c0 / BT]));
+          }
+          if (!move_to(mc) || !wait_pv()) {
+            ok = false;
+            break;
+          }
+          const float base = (m == p_neg_inf()) ? 0.f : m;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kChunk; c0 += 8) {
+            const float lv = sm.lv[st][c0 / BT];
+            float x[8], sum = 0.f;
+            load8(c0, x);
+            uint32_t w[4];
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+              const float e0 = p_exp2(fmaf(x[c], sc.x, lv - base));
+              const float e1 = p_exp2(fmaf(x[c + 1], sc.x, lv - base));
+              sum += e0 + e1;
+              w[c >> 1] = pack_f16(e0, e1);
+            }
+            tc::tmem_st4(p_addr + c0 / 2, w);
+            l = fmaf(sum, p_exp2(-lv), l);
+          }
+          tc::fence_before_sync();
+          mbar_arrive(&sm.s_free[h]);
         }
-        tc::tmem_st32(p_addr, *reinterpret_cast<uint32_t(*)[32]>(&pw[0]));
-        tc::tmem_st32(p_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[32]));
-        l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
         tc::tmem_st_wait();
         tc::fence_before_sync();    // P, for the tensor core
         mbar_arrive(&sm.p_full[h]);
@@ -608,11 +818,6 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       mbar_arrive(&sm.o_free[h]);   // the next item's first PV may clear O
-      if (sm.nan_any[qb]) {   // a NaN value among the item's last keys: for the rows that see it
-#pragma unroll
-        for (int d = 0; d < kD; ++d)
-          if (sm.nan_from[qb][d] <= qpos) ov[d] = 0x7fffffffu;
-      }
       const float inv = (l > 0.f) ? 1.f / l : 0.f;
       auto row_chunk = [&](int e) {
         const float *f = reinterpret_cast<const float *>(&ov[8 * e]);
@@ -630,6 +835,11 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
 #pragma unroll
         for (int e = 0; e < kD / 8; ++e)
           *reinterpret_cast<uint4 *>(stg + ((e ^ (r & 7)) << 4)) = row_chunk(e);
+        if (sm.nan_any[qb])   // NaN values that the row sees among the item's last keys
+#pragma unroll 1
+          for (int d = 0; d < kD; ++d)
+            if (sm.nan_from[qb][d] <= qpos)
+              *reinterpret_cast<uint16_t *>(stg + (((d >> 3) ^ (r & 7)) << 4) + 2 * (d & 7)) = 0x7fc0;
         fence_proxy_async_smem();
         mbar_arrive(&sm.staged[h]);
         if (r == 0) {
@@ -649,6 +859,10 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
                        it.g * kGqa + hh) * kD);
 #pragma unroll
           for (int e = 0; e < kD / 8; ++e) dst[e] = row_chunk(e);
+          if (sm.nan_any[qb])
+#pragma unroll 1
+            for (int d = 0; d < kD; ++d)
+              if (sm.nan_from[qb][d] <= qpos) reinterpret_cast<uint16_t *>(dst)[d] = 0x7fc0;
         }
         // the buffer's NaN record is read by every row before it is released
         mbar_arrive(&sm.staged[h]);

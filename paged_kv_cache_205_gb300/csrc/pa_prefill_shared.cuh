@@ -236,7 +236,7 @@ struct PageGeom {
 // chunk is refused have none), and, up to kSortTiles tiles, their order by
 // weight (sm.order).  Every thread of the CTA calls it; returns the number of
 // tiles.
-template <int BT, int kThreads, class Sm>
+template <int BT, int kThreads, int kSort, class Sm>
 __device__ __forceinline__ int order_tiles(Sm &sm, const PrefillParams &p, int tid, int warp,
                                            int lane) {
   const long long cap = static_cast<long long>(p.max_blocks) * BT;
@@ -280,7 +280,7 @@ __device__ __forceinline__ int order_tiles(Sm &sm, const PrefillParams &p, int t
   if (static_cast<int>(blockIdx.x) >= total_tiles * kHkv) return total_tiles;
 
   // ---- the tiles heaviest first: a stable counting sort by weight
-  const bool sorted = total_tiles <= kSortTiles;
+  const bool sorted = total_tiles <= kSort;
   if (sorted) {
     for (int b = tid; b < kWeightBins; b += kThreads) sm.bin_start[b] = 0;
     __syncthreads();
