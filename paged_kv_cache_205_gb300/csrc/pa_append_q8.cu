@@ -7,9 +7,8 @@
 //                            k and v to the page's scale; where the new token
 //                            needs a larger scale than the page has, the
 //                            page's earlier tokens are brought to it.
-//   prefill_store_q8_kernel  one CTA per window of BT packed rows: the runs of
-//                            rows that fall into one page ("segments", as a
-//                            rule one) are taken in turn; a segment's values
+//   prefill_store_q8_kernel  one CTA per page that the call's rows touch, half
+//                            its warps on k and v, half on q; a page's values
 //                            stay in registers between the maximum that sets
 //                            the scale and the rounding.
 // Both are bound by memory (large) or latency (small): a row costs 2 KiB of k
@@ -138,222 +137,252 @@ __global__ void __launch_bounds__(kStoreQ8Threads) append_store_q8_kernel(Append
 }
 
 // ------------------------------------------------------------------ prefill
+// (cos, sin) of a row's 32 pairs: thread c of a head row takes pairs 8c..8c+7,
+// two at a time; pairs 8c + 2w and 8c + 2w + 1 lie at [4w + c], so that the four
+// threads of a row read 64 consecutive bytes.
+struct __align__(16) RowAngles {
+  float4 a[kD / 4];
+  __device__ __forceinline__ void set(int d, float2 cs) {
+    const int c = d >> 3, w = (d >> 1) & 3;
+    reinterpret_cast<float2 *>(&a[4 * w + c])[d & 1] = cs;
+  }
+};
+
+// The pairs (lo, hi) of one bf16 word each, rotated by (x, y) and (z, w).
+__device__ __forceinline__ void rotate2(uint32_t *lo, uint32_t *hi, float4 cs) {
+  const float2 a = bf16x2_to_float2(*lo), b = bf16x2_to_float2(*hi);
+  *lo = float_to_bf16_bits(fmaf(a.x, cs.x, -b.x * cs.y)) |
+        (float_to_bf16_bits(fmaf(a.y, cs.z, -b.y * cs.w)) << 16);
+  *hi = float_to_bf16_bits(fmaf(b.x, cs.x, a.x * cs.y)) |
+        (float_to_bf16_bits(fmaf(b.y, cs.z, a.y * cs.w)) << 16);
+}
+
 // 16 bytes (8 bf16) of one half of a head row, rotated against the other half.
-__device__ __forceinline__ void rotate8(uint4 *lo, uint4 *hi, const float2 *cs, int c) {
-  uint2 l0 = make_uint2(lo->x, lo->y), l1 = make_uint2(lo->z, lo->w);
-  uint2 h0 = make_uint2(hi->x, hi->y), h1 = make_uint2(hi->z, hi->w);
-  rotate4(l0, h0, cs, 2 * c, &l0, &h0);
-  rotate4(l1, h1, cs, 2 * c + 1, &l1, &h1);
-  *lo = make_uint4(l0.x, l0.y, l1.x, l1.y);
-  *hi = make_uint4(h0.x, h0.y, h1.x, h1.y);
+__device__ __forceinline__ void rotate8(uint4 *lo, uint4 *hi, const RowAngles &r, int c) {
+  rotate2(&lo->x, &hi->x, r.a[c]);
+  rotate2(&lo->y, &hi->y, r.a[4 + c]);
+  rotate2(&lo->z, &hi->z, r.a[8 + c]);
+  rotate2(&lo->w, &hi->w, r.a[12 + c]);
 }
 
 __device__ __forceinline__ uint32_t q8_top4(uint4 w, uint32_t top) {
   return q8_top(w.w, q8_top(w.z, q8_top(w.y, q8_top(w.x, top))));
 }
 
-// Threads of the prefill store: 32 (4 per kv head) for each row of a pass.
+// A CTA takes the rows of one call that fall into one page.  Sequence s owns
+// CTAs cu_tokens[s] / BT + 2 s and up: n rows touch at most n / BT + 2 pages, so
+// the ranges do not meet, and total_tokens / BT + 2 num_seqs CTAs hold them all.
+// Half its warps take k and v (two rows of each a warp, held in registers
+// between the maximum that sets the scale and the rounding), half q; the angles
+// (fp64, a tenth of the instructions but a quarter of the time on that pipe) are
+// worked out once for both.  64 registers let two CTAs of 512 threads, 128 KiB of
+// loads, be on the way per SM.  8 x 2048 tokens take 36.5 us, 184 MB at 5.1 TB/s
+// (a CTA per window of rows with every warp on k, v and q in turn, 104 registers
+// and one CTA an SM: 53 us); 31 tokens 8.9 us, the allocation and the loads one
+// after another.
 template <int BT>
 struct StoreGeom {
-  static constexpr int kThreads = BT == 8 ? 256 : 512;
-  static constexpr int kPassRows = kThreads / 32;        // rows of k (and of v) a pass takes
-  static constexpr int kPasses = BT / kPassRows;         // 1, 1, 2
-  static constexpr int kQItems = BT * kHq * 4 / kThreads;   // 4, 4, 8 parts of q rows a thread
+  static constexpr int kThreads = 32 * BT;
+  static constexpr int kRole = kThreads / 2;         // threads for k and v, threads for q
+  static constexpr int kPassRows = kRole / 32;       // 4 threads per kv head and row
+  static constexpr int kPasses = 2;
+  static constexpr int kQBatch = 4;                  // parts of q rows a thread holds
+  static constexpr int kQBatches = 2;
+  static_assert(kPassRows * kPasses == BT && kRole * kQBatch * kQBatches == BT * kHq * 4, "");
 };
 
 template <int BT>
-__global__ void __launch_bounds__(StoreGeom<BT>::kThreads) prefill_store_q8_kernel(
-    PrefillAppendParams p, Q8Out o) {
+__global__ void __launch_bounds__(StoreGeom<BT>::kThreads, 1024 / StoreGeom<BT>::kThreads)
+prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o) {
   using G = StoreGeom<BT>;
   constexpr size_t kHalfPage = static_cast<size_t>(BT) * kQ8TokBytes;
-  __shared__ float2 cs[BT][kD / 2];
-  __shared__ int row_seq[BT], row_pos[BT], row_len[BT];
-  __shared__ uint32_t starts_s;
+  __shared__ RowAngles cs[BT];
+  __shared__ int owner_s, ctx_s, n_s, row0_s;   // the sequence, its context, rows and first row
   __shared__ uint32_t top_s[2][kHkv];
   __shared__ int e_s[2][kHkv], held_s[2][kHkv];   // held: exponent of the page's scale so far
   __shared__ int blk_s;
   pdl_launch_dependents();   // the next kernel may start its own set-up
   const int tid = threadIdx.x;
-  const int r0 = blockIdx.x * BT;
-  // lane i: row r0 + i's sequence (the largest s with cu_tokens[s] <= r: an
-  // empty chunk's start equals the next one's, so the search passes over it),
-  // position, and whether a segment (a run of rows in one page) starts there
-  if (tid < 32) {
-    bool start = false;
-    if (tid < BT) {
-      const int r = r0 + tid;
-      int seq = 0, pos = 0, len = 0;
-      if (r < p.total_tokens) {
-        int lo = 0, hi = p.num_seqs - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (p.cu_tokens[mid] <= r) lo = mid;
-          else hi = mid - 1;
-        }
-        int ctx, n;
-        const int c0 = p.cu_tokens[lo], c1 = p.cu_tokens[lo + 1];
-        // a refused chunk is reported by the allocation kernel
-        if (chunk_fits<BT>(p, lo, &ctx, &n) && r >= c0 && r < c1) {
-          seq = lo;
-          pos = ctx + (r - c0);
-          start = r == c0 || pos % BT == 0;
-          len = min(BT - pos % BT, c1 - r);
-        }
-      }
-      row_seq[tid] = seq;
-      row_pos[tid] = pos;
-      row_len[tid] = len;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, start);
-    if (tid == 0) starts_s = m;
+  if (tid == 0) owner_s = -1;
+  if (tid < 2 * kHkv) top_s[tid >> 3][tid & 7] = 0u;
+  __syncthreads();
+  int mine = -1, my_ctx = 0, my_n = 0;
+  for (int s = tid; s < p.num_seqs; s += G::kThreads) {
+    int ctx, n;
+    // (a refused chunk is reported by the allocation kernel)
+    if (!chunk_fits<BT>(p, s, &ctx, &n) || n == 0) continue;
+    const long long j = static_cast<long long>(blockIdx.x) - (p.cu_tokens[s] / BT + 2ll * s);
+    if (j < 0 || j > (ctx + n - 1) / BT - ctx / BT) continue;
+    mine = s;
+    my_ctx = ctx;
+    my_n = n;
+  }
+  // (more than one claim only where cu_tokens decreases somewhere)
+  if (mine >= 0) atomicMax(&owner_s, mine);
+  __syncthreads();
+  const int seq = owner_s;
+  if (seq < 0) {
+    pdl_wait_primary();   // this grid ends after the allocation kernel
+    return;
+  }
+  if (mine == seq) {
+    ctx_s = my_ctx;
+    n_s = my_n;
+    row0_s = p.cu_tokens[seq];
   }
   __syncthreads();
-  const int krow = tid >> 5, khead = (tid >> 2) & 7, c = tid & 3;
-  for (unsigned left = starts_s; left; left &= left - 1) {
-    const int at = __ffs(left) - 1;
-    const int len = row_len[at], pos0 = row_pos[at], seq = row_seq[at];
-    const size_t first = static_cast<size_t>(r0) + at;
-    // every load of the segment is in flight before anything waits on one
-    uint4 klo[G::kPasses], khi[G::kPasses], v0[G::kPasses], v1[G::kPasses];
-    uint32_t top_k = 0, top_v = 0;
+  const int ctx = ctx_s;
+  const int page_at = ctx / BT + static_cast<int>(blockIdx.x) - (row0_s / BT + 2 * seq);
+  const int pos0 = max(ctx, page_at * BT);
+  const int len = min(ctx + n_s, page_at * BT + BT) - pos0;
+  const size_t first = static_cast<size_t>(row0_s) + (pos0 - ctx);   // packed row of pos0
+  const int c = tid & 3;
+  auto angles = [&]() {   // one pair a thread
+    const int t = tid / (kD / 2), d = tid % (kD / 2);
+    if (t < len) cs[t].set(d, rope_cos_sin(pos0 + t, p.freqs.f[d]));
+  };
+
+  if (tid >= G::kRole) {
+    // ------------------------------------------------------------------- q
+    const int qt = tid - G::kRole;
+    uint4 lo[G::kQBatch], hi[G::kQBatch];
+    auto q_at = [&](int i) -> size_t {   // item i of the thread: row, head, part c
+      const int item = qt + i * G::kRole;
+      return ((first + (item >> 7)) * kHq + ((item >> 2) & 31)) * kD + 8 * c;
+    };
+    auto held = [&](int i) { return p.q && ((qt + i * G::kRole) >> 7) < len; };
+    auto load = [&](int base) {
+#pragma unroll
+      for (int i = 0; i < G::kQBatch; ++i) {
+        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+        if (held(base + i)) {
+          const uint16_t *row = p.q + q_at(base + i);
+          lo[i] = *reinterpret_cast<const uint4 *>(row);
+          hi[i] = *reinterpret_cast<const uint4 *>(row + kD / 2);
+        }
+      }
+    };
+    load(0);
+    angles();
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < G::kQBatches; ++b) {
+      if (b > 0) load(b * G::kQBatch);
+#pragma unroll
+      for (int i = 0; i < G::kQBatch; ++i) {
+        const int it = b * G::kQBatch + i;
+        if (!held(it)) continue;
+        rotate8(&lo[i], &hi[i], cs[(qt + it * G::kRole) >> 7], c);
+        uint16_t *row = o.q_out + q_at(it);
+        *reinterpret_cast<uint4 *>(row) = lo[i];
+        *reinterpret_cast<uint4 *>(row + kD / 2) = hi[i];
+      }
+    }
+    pdl_wait_primary();
+    return;
+  }
+
+  // -------------------------------------------------------------- k and v
+  const int krow = tid >> 5, khead = (tid >> 2) & 7;
+  uint4 klo[G::kPasses], khi[G::kPasses], v0[G::kPasses], v1[G::kPasses];
+#pragma unroll
+  for (int i = 0; i < G::kPasses; ++i) {
+    const int t = krow + i * G::kPassRows;
+    klo[i] = khi[i] = v0[i] = v1[i] = make_uint4(0, 0, 0, 0);
+    if (t < len) {
+      const size_t row = ((first + t) * kHkv + khead) * kD;
+      klo[i] = *reinterpret_cast<const uint4 *>(p.k_new + row + 8 * c);
+      khi[i] = *reinterpret_cast<const uint4 *>(p.k_new + row + kD / 2 + 8 * c);
+      v0[i] = *reinterpret_cast<const uint4 *>(p.v_new + row + 16 * c);
+      v1[i] = *reinterpret_cast<const uint4 *>(p.v_new + row + 16 * c + 8);
+    }
+  }
+  angles();
+  // ---- the largest magnitudes of each head's keys (before the rotation) and values
+  uint32_t top_k = 0, top_v = 0;
+#pragma unroll
+  for (int i = 0; i < G::kPasses; ++i) {
+    top_k = q8_top4(khi[i], q8_top4(klo[i], top_k));
+    top_v = q8_top4(v1[i], q8_top4(v0[i], top_v));
+  }
+  top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, 1));
+  top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, 2));
+  top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, 1));
+  top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, 2));
+  if (c == 0) {
+    atomicMax(&top_s[0][khead], top_k);
+    atomicMax(&top_s[1][khead], top_v);
+  }
+  __syncthreads();
+  // ---- the page and its scales
+  const int slot0 = pos0 % BT;
+  if (tid < 2 * kHkv) {
+    const bool opened = slot0 == 0;   // this call opens the page
+    if (opened) pdl_wait_primary();   // its entry comes from the allocation kernel
+    const int blk = p.block_table[table_row(seq, p.n_layers, p.layer, p.max_blocks) + page_at];
+    const bool ok = blk >= 0 && blk < p.num_blocks;
+    const int kv = tid >> 3, h = tid & 7;
+    int e = q8_exponent(top_s[kv][h], kv ? kMantV : kMantK), held = e;
+    if (ok) {
+      float *scale = o.scales + (static_cast<size_t>(blk) * 2 + kv) * kHkv + h;
+      if (!opened) {
+        held = q8_scale_exponent(*scale);
+        if (held < kMinExp) report(p.err, PA_DEV_BAD_SCALE);
+        e = max(e, held);
+      }
+      if (held >= kMinExp) *scale = pow2(e);
+    } else if (!opened && tid == 0) {
+      // a page of this chunk that was refused or popped invalid is reported
+      // by the allocation kernel; an invalid page from before is reported here
+      report(p.err, PA_DEV_BAD_BLOCK);
+    }
+    e_s[kv][h] = e;
+    held_s[kv][h] = held;
+    if (tid == 0) blk_s = ok ? blk : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < G::kPasses; ++i) {   // (meanwhile)
+    const int t = krow + i * G::kPassRows;
+    if (t < len) rotate8(&klo[i], &khi[i], cs[t], c);
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(G::kRole) : "memory");
+  if (blk_s >= 0) {
+    unsigned char *page = p.kv + static_cast<size_t>(blk_s) * 2 * kHalfPage;
+    // ---- tokens that the page holds already are brought to its new scale
+    for (int x = tid; x < slot0 * 64; x += G::kRole) {   // 16-byte parts: 32 of K, 32 of V a token
+      const int t = x >> 6, kv = (x >> 5) & 1, part = x & 31, h = part >> 2;
+      const int held = held_s[kv][h], e = e_s[kv][h];
+      if (held < kMinExp || held == e) continue;
+      const float ratio = pow2(max(held - e, -126));
+      uint4 *w = reinterpret_cast<uint4 *>(page + kv * kHalfPage + t * kQ8TokBytes + 16 * part);
+      uint4 u = *w;
+      u.x = e4m3x4_rescale(u.x, ratio);
+      u.y = e4m3x4_rescale(u.y, ratio);
+      u.z = e4m3x4_rescale(u.z, ratio);
+      u.w = e4m3x4_rescale(u.w, ratio);
+      *w = u;
+    }
+    const float inv_k = pow2(-e_s[0][khead]), inv_v = pow2(-e_s[1][khead]);
 #pragma unroll
     for (int i = 0; i < G::kPasses; ++i) {
       const int t = krow + i * G::kPassRows;
-      klo[i] = khi[i] = v0[i] = v1[i] = make_uint4(0, 0, 0, 0);
-      if (t < len) {
-        const size_t row = ((first + t) * kHkv + khead) * kD;
-        klo[i] = *reinterpret_cast<const uint4 *>(p.k_new + row + 8 * c);
-        khi[i] = *reinterpret_cast<const uint4 *>(p.k_new + row + kD / 2 + 8 * c);
-        v0[i] = *reinterpret_cast<const uint4 *>(p.v_new + row + 16 * c);
-        v1[i] = *reinterpret_cast<const uint4 *>(p.v_new + row + 16 * c + 8);
+      if (t >= len) continue;
+      unsigned char *row = page + (slot0 + t) * kQ8TokBytes + khead * kQ8HeadBytes;
+      if (held_s[0][khead] >= kMinExp) {
+        *reinterpret_cast<uint2 *>(row + 8 * c) =
+            make_uint2(bf16x4_to_e4m3x4(klo[i].x, klo[i].y, inv_k),
+                       bf16x4_to_e4m3x4(klo[i].z, klo[i].w, inv_k));
+        *reinterpret_cast<uint2 *>(row + kD / 2 + 8 * c) =
+            make_uint2(bf16x4_to_e4m3x4(khi[i].x, khi[i].y, inv_k),
+                       bf16x4_to_e4m3x4(khi[i].z, khi[i].w, inv_k));
       }
+      if (held_s[1][khead] >= kMinExp)
+        *reinterpret_cast<uint4 *>(row + kHalfPage + 16 * c) =
+            make_uint4(bf16x4_to_e4m3x4(v0[i].x, v0[i].y, inv_v),
+                       bf16x4_to_e4m3x4(v0[i].z, v0[i].w, inv_v),
+                       bf16x4_to_e4m3x4(v1[i].x, v1[i].y, inv_v),
+                       bf16x4_to_e4m3x4(v1[i].z, v1[i].w, inv_v));
     }
-    uint4 qlo[4], qhi[4];
-    auto load_q = [&](int base) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int item = tid + (base + i) * G::kThreads;
-        const int t = item >> 7, h = (item >> 2) & 31;
-        qlo[i] = qhi[i] = make_uint4(0, 0, 0, 0);
-        if (p.q && t < len) {
-          const uint16_t *row = p.q + ((first + t) * kHq + h) * kD;
-          qlo[i] = *reinterpret_cast<const uint4 *>(row + 8 * c);
-          qhi[i] = *reinterpret_cast<const uint4 *>(row + kD / 2 + 8 * c);
-        }
-      }
-    };
-    auto store_q = [&](int base) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int item = tid + (base + i) * G::kThreads;
-        const int t = item >> 7, h = (item >> 2) & 31;
-        if (p.q && t < len) {
-          rotate8(&qlo[i], &qhi[i], cs[t], c);
-          uint16_t *row = o.q_out + ((first + t) * kHq + h) * kD;
-          *reinterpret_cast<uint4 *>(row + 8 * c) = qlo[i];
-          *reinterpret_cast<uint4 *>(row + kD / 2 + 8 * c) = qhi[i];
-        }
-      }
-    };
-    load_q(0);
-    if (tid < 2 * kHkv) top_s[tid >> 3][tid & 7] = 0u;
-    for (int x = tid; x < len * (kD / 2); x += G::kThreads) {
-      const int t = x / (kD / 2), d = x % (kD / 2);
-      cs[t][d] = rope_cos_sin(pos0 + t, p.freqs.f[d]);
-    }
-    __syncthreads();
-    // ---- the largest magnitudes of each head's keys and values
-#pragma unroll
-    for (int i = 0; i < G::kPasses; ++i) {
-      top_k = q8_top4(khi[i], q8_top4(klo[i], top_k));
-      top_v = q8_top4(v1[i], q8_top4(v0[i], top_v));
-    }
-    top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, 1));
-    top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, 2));
-    top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, 1));
-    top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, 2));
-    if (c == 0) {
-      atomicMax(&top_s[0][khead], top_k);
-      atomicMax(&top_s[1][khead], top_v);
-    }
-    // (q of the first rows while the table is read)
-    store_q(0);
-    __syncthreads();
-    // ---- the page and its scales
-    const int slot0 = pos0 % BT;
-    if (tid < 2 * kHkv) {
-      const bool opened = slot0 == 0;   // this call opens the page
-      if (opened) pdl_wait_primary();   // its entry comes from the allocation kernel
-      const int blk =
-          p.block_table[table_row(seq, p.n_layers, p.layer, p.max_blocks) + pos0 / BT];
-      const bool ok = blk >= 0 && blk < p.num_blocks;
-      const int kv = tid >> 3, h = tid & 7;
-      int e = q8_exponent(top_s[kv][h], kv ? kMantV : kMantK), held = e;
-      if (ok) {
-        float *scale = o.scales + (static_cast<size_t>(blk) * 2 + kv) * kHkv + h;
-        if (!opened) {
-          held = q8_scale_exponent(*scale);
-          if (held < kMinExp) report(p.err, PA_DEV_BAD_SCALE);
-          e = max(e, held);
-        }
-        if (held >= kMinExp) *scale = pow2(e);
-      } else if (!opened && tid == 0) {
-        // a page of this chunk that was refused or popped invalid is reported
-        // by the allocation kernel; an invalid page from before is reported here
-        report(p.err, PA_DEV_BAD_BLOCK);
-      }
-      e_s[kv][h] = e;
-      held_s[kv][h] = held;
-      if (tid == 0) blk_s = ok ? blk : -1;
-    }
-    __syncthreads();
-    if (blk_s >= 0) {
-      unsigned char *page = p.kv + static_cast<size_t>(blk_s) * 2 * kHalfPage;
-      // ---- tokens that the page holds already are brought to its new scale
-      if (slot0 != 0) {
-        for (int x = tid; x < slot0 * 64; x += G::kThreads) {   // 16-byte parts: 32 of K, 32 of V a token
-          const int t = x >> 6, kv = (x >> 5) & 1, part = x & 31, h = part >> 2;
-          const int held = held_s[kv][h], e = e_s[kv][h];
-          if (held < kMinExp || held == e) continue;
-          const float ratio = pow2(max(held - e, -126));
-          uint4 *w = reinterpret_cast<uint4 *>(page + kv * kHalfPage + t * kQ8TokBytes + 16 * part);
-          uint4 u = *w;
-          u.x = e4m3x4_rescale(u.x, ratio);
-          u.y = e4m3x4_rescale(u.y, ratio);
-          u.z = e4m3x4_rescale(u.z, ratio);
-          u.w = e4m3x4_rescale(u.w, ratio);
-          *w = u;
-        }
-      }
-      const float inv_k = pow2(-e_s[0][khead]), inv_v = pow2(-e_s[1][khead]);
-#pragma unroll
-      for (int i = 0; i < G::kPasses; ++i) {
-        const int t = krow + i * G::kPassRows;
-        if (t >= len) continue;
-        unsigned char *row = page + (slot0 + t) * kQ8TokBytes + khead * kQ8HeadBytes;
-        if (held_s[0][khead] >= kMinExp) {
-          rotate8(&klo[i], &khi[i], cs[t], c);
-          *reinterpret_cast<uint2 *>(row + 8 * c) =
-              make_uint2(bf16x4_to_e4m3x4(klo[i].x, klo[i].y, inv_k),
-                         bf16x4_to_e4m3x4(klo[i].z, klo[i].w, inv_k));
-          *reinterpret_cast<uint2 *>(row + kD / 2 + 8 * c) =
-              make_uint2(bf16x4_to_e4m3x4(khi[i].x, khi[i].y, inv_k),
-                         bf16x4_to_e4m3x4(khi[i].z, khi[i].w, inv_k));
-        }
-        if (held_s[1][khead] >= kMinExp)
-          *reinterpret_cast<uint4 *>(row + kHalfPage + 16 * c) =
-              make_uint4(bf16x4_to_e4m3x4(v0[i].x, v0[i].y, inv_v),
-                         bf16x4_to_e4m3x4(v0[i].z, v0[i].w, inv_v),
-                         bf16x4_to_e4m3x4(v1[i].x, v1[i].y, inv_v),
-                         bf16x4_to_e4m3x4(v1[i].z, v1[i].w, inv_v));
-      }
-    }
-#pragma unroll
-    for (int base = 4; base < G::kQItems; base += 4) {
-      load_q(base);
-      store_q(base);
-    }
-    __syncthreads();   // cs, top_s and the exponents are reused
   }
   pdl_wait_primary();   // this grid ends after the allocation kernel
 }
@@ -425,6 +454,7 @@ int prefill_append_q8_impl(const uint16_t *k_new, const uint16_t *v_new, const u
     return PA_ERR_ARG;
   if (static_cast<long long>(max_blocks_per_seq) * BT > INT_MAX) return PA_ERR_ARG;
   if (layer < 0 || layer >= n_layers) return PA_ERR_LAYER;
+  if (num_seqs > (1 << 29)) return PA_ERR_ARG;   // the grid, total_tokens / BT + 2 num_seqs
   if (num_seqs == 0 || total_tokens == 0) return PA_OK;
   if (!k_new || !v_new || !cu_tokens || !kv_cache || !kv_scales || !block_table ||
       !context_lens || !free_list || !free_count || !err || (q_or_null && !q_out))
@@ -458,7 +488,7 @@ int prefill_append_q8_impl(const uint16_t *k_new, const uint16_t *v_new, const u
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (launch_pdl(prefill_alloc_kernel<BT>, dim3(1), dim3(kScanCta), 0, st, prm) != cudaSuccess)
     return PA_ERR_CUDA;
-  if (launch_pdl(prefill_store_q8_kernel<BT>, dim3((total_tokens + BT - 1) / BT),
+  if (launch_pdl(prefill_store_q8_kernel<BT>, dim3(total_tokens / BT + 2 * num_seqs),
                  dim3(StoreGeom<BT>::kThreads), 0, st, prm, o) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
