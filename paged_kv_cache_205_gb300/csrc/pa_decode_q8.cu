@@ -451,8 +451,8 @@ template <int BT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_q8_kernel(const __grid_constant__ CUtensorMap kv_map, Q8DecodeParams p) {
   extern __shared__ unsigned char smem_raw[];
-  Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                       ~static_cast<uintptr_t>(1023));
+  // (an offset, so that the compiler still knows it for shared memory)
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw + (-smem_u32(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = gridDim.x;
   if (tid == 0) {

@@ -17,7 +17,7 @@
 // the softmax is
 //   y = s * (f sK) + log2 sV - M     (one FMA, as for the bf16 cache)
 //   P = 2^y,  O = sum P V16,  l = sum P / sV
-// with f the item's score factor and M a reference 2^7 below the row's largest
+// with f the row's score factor and M a reference 2^7 below the row's largest
 // s f sK + log2 sV, which moves when a chunk exceeds it by more than 2^15: M
 // follows the weights times the values' scale, so that P fits f16 (<= 2^15)
 // however far the scales lie apart.  f16 rounds a P by half a step, 2^-12 of it or
@@ -26,9 +26,21 @@
 // log2 sV page by page, so that a heavy key in a page of small scale does not lift
 // the reference by the others' scale.  (K's scales may lie any distance apart: f16
 // takes a factor down to 2^-15 without rounding, and what is lost below weighs
-// 2^-33 of the largest key's score.)  The converter also turns an item's q
-// into f16, scaled by a power of two (f undoes it), exact for values down to
-// 2^-29 of the item's largest.
+// 2^-33 of the largest key's score.)
+// The converter also turns q into f16, a row scaled by a power of two (f undoes
+// it), exact for values down to 2^-29 of the row's largest.
+//
+// What bounds it: the instructions issued (the issue slots are 55% busy, with the
+// conversion or, in the bf16 kernel, without it).  So the work is laid out to
+// issue little: one thread, the producer's lane 0, works an item out and hands it
+// on with q (each softmax and MMA warp for itself: 229 / 765 us), and the
+// converter's loop skips the multiplication where a page's factor is 1 and the
+// masks in chunks that need none, and stays rolled (unrolled it runs in bursts
+// against the softmax warps: 240 / 790 us).  8 x 2048 tokens 223 us, 617 TFLOP/s
+// (the bf16 kernel over the same values 186), 32 x 512 after 4096 747 us, 782
+// TFLOP/s (629).  Tried and slower: K's bytes as the tensor core's own e4m3 operand
+// against q in two e4m3 parts, which halves the converter's work but leaves the
+// pages' K scales to the softmax, whose registers they outgrow (267 / 815 us).
 #include "pa_prefill_shared.cuh"
 #include "pa_q8.cuh"
 #include <cuda_fp16.h>
@@ -48,8 +60,8 @@ constexpr float kTiny = 1.2e-38f;
 // Register budget: 512 threads x 128 at launch; the softmax warpgroups take
 // kQRegsSoft, the producer/MMA warpgroup and the converters give up to theirs.
 constexpr int kQRegsSoft = 192;
-constexpr int kQRegsMma = 80;
-constexpr int kQRegsConv = 48;
+constexpr int kQRegsMma = 72;
+constexpr int kQRegsConv = 56;
 static_assert(128 * (2 * kQRegsSoft + kQRegsMma + kQRegsConv) <= kQThreads * 128,
               "register split above the launch budget");
 
@@ -62,10 +74,18 @@ struct __align__(16) RawChunk {
   float sk;      // the chunk's K scale
   float lv;      // log2 of its V scale
 };
+// An item as the producer hands it to the MMA and softmax warps, with its q.
+struct __align__(16) ItemRec {
+  int ctx, row0, t0, g;
+  int rows0, rows1;   // query tokens of half 0 / half 1 (<= 0: no work)
+  int n_chunks, nc0;  // 128-key chunks: the tile's (0: no more items), half 0's
+  __device__ __forceinline__ int nc1() const { return rows1 > 0 ? n_chunks : 0; }
+};
 constexpr int kFirst = 1;       // the item's first chunk: its q comes with it
 constexpr int kTwoHalves = 2;
 constexpr int kDiagonal = 4;    // some row of the tile does not see some key
 constexpr int kFarApart = 8;    // V's scales spread over more than 2^7
+constexpr int kMasked = 32;     // a key past the tile's last, or a page not loaded
 constexpr int kEnd = 16;        // no more chunks
 
 struct __align__(1024) QSmem {
@@ -80,12 +100,14 @@ struct __align__(1024) QSmem {
   uint2 raw_mul[kRaw][kChunk / 8];                 // per page: f16x2 factors of K's and V's bytes
   float raw_lv[kRaw][kChunk / 8];                  // per page: log2 of V's scale
   RawChunk raw_rec[kRaw];
-  float4 scale[kWide];                             // (f sK, log2 sV, 1 / sV, 1: V's pages far apart)
+  ItemRec item[kQBufs];
+  float4 scale[kWide];                             // (sK, log2 sV, 1 / sV, 1: V's pages far apart)
   float lv[kWide][kChunk / 8];                     // far apart: log2 of V's scale per page
-  uint32_t q_top[4];                               // the converter warps' largest |q| (bf16 pattern)
-  int nan_from[kQBufs][kD];                        // per dim: first position of the item's diagonal
-                                                   // chunks whose value is NaN
-  int nan_any[kQBufs];                             // some nan_from is set
+  uint8_t q_exp[kQBufs][kHalves][kRows];           // per row: exponent field of its largest |q|
+  // per dim: the first position in an item's diagonal chunks whose value is NaN,
+  // below the item's number inverted (a later item's record is the smaller one)
+  unsigned long long nan_from[kQBufs][kD];
+  int nan_item[kQBufs];                            // the last item with such a record
   uint64_t q_full[kQBufs];
   uint64_t q_ready[kQBufs];                        // q is f16
   uint64_t q_empty[kQBufs];
@@ -107,18 +129,6 @@ struct __align__(1024) QSmem {
 
 static_assert(sizeof(QSmem) + 1024 <= 227 * 1024, "shared memory above the per-CTA limit");
 
-// Two packed e4m3 times mul (two f16).
-__device__ __forceinline__ uint32_t widen2(uint32_t pair, uint32_t mul) {
-  const uint32_t h = e4m3x2_to_f16x2(pair);
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(mul));
-  return r;
-}
-// 8 e4m3 values times mul as f16.
-__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t mul) {
-  return make_uint4(widen2(a, mul), widen2(a >> 16, mul), widen2(b, mul), widen2(b >> 16, mul));
-}
-
 // Two f16 2^d (d <= 0; 0 below f16's smallest number).
 __device__ __forceinline__ uint32_t pow2_f16x2(int d) {
   const uint32_t h = d >= -14 ? static_cast<uint32_t>(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
@@ -128,6 +138,33 @@ __device__ __forceinline__ uint32_t pow2_f16x2(int d) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
+  return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b),
+                    e4m3x2_to_f16x2(b >> 16));
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint4 mul8(uint4 a, uint32_t m) {
+  return make_uint4(mul2(a.x, m), mul2(a.y, m), mul2(a.z, m), mul2(a.w, m));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // The largest |q| (bf16 pattern) of row r of a half's q tile (128-byte rows,
@@ -142,6 +179,10 @@ __device__ __forceinline__ uint32_t q_row_top(const unsigned char *row, int r) {
   }
   return max(top & 0xffffu, top >> 16);
 }
+
+// Exponent field of the power of two that brings a row whose largest |q| has
+// exponent field e to [2^12, 2^13).
+__device__ __forceinline__ int q_scale_field(int e) { return min(266 - e, 253); }
 
 // The row from bf16 to f16 in place, times `up`.
 __device__ __forceinline__ void q_row_to_f16(unsigned char *row, int r, float up) {
@@ -161,30 +202,23 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// w with its NaN bytes (`nan`, from nan_bytes) replaced by zeros; from[d] takes
-// the position of a NaN in dim d when it is the first.  Rare.
-__device__ __forceinline__ uint32_t without_nan(uint32_t w, int dim0, int pos, int *from) {
+// w with its NaN bytes replaced by zeros; from[d] takes the position of a NaN
+// in dim d when it is the item's first.  Rare.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w, int dim0, int item, int pos,
+                                                unsigned long long *from) {
   for (uint32_t m = nan_bytes(w); m; m &= m - 1) {
     const int byte = (__ffs(m) - 1) >> 3;
     w &= ~(0xffu << (8 * byte));
-    atomicMin(from + dim0 + byte, pos);
+    atomicMin(from + dim0 + byte,
+              (static_cast<unsigned long long>(~static_cast<uint32_t>(item)) << 32) | pos);
   }
   return w;
 }
 
-// Whether `mine` holds in all converter threads (a barrier among them: they take
-// the same way past a wait that ran out in some).
-__device__ __forceinline__ bool converters_agree(bool mine) {
-  int all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.s32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
-      "selp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(mine ? 1 : 0), "n"(kConvThreads)
-      : "memory");
-  return all != 0;
+// Whether a dim with record `from` is NaN for the row at qpos of item k.
+__device__ __forceinline__ bool sees_nan(unsigned long long from, int k, int qpos) {
+  return static_cast<uint32_t>(from >> 32) == ~static_cast<uint32_t>(k) &&
+         static_cast<uint32_t>(from) <= static_cast<uint32_t>(qpos);
 }
 
 // MMA warp: waits until chunk gc is widened (every MMA warp does, for every
@@ -229,9 +263,11 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
     const __grid_constant__ CUtensorMap out_map, PrefillParams p,
     const float *__restrict__ scales) {
   extern __shared__ unsigned char smem_raw[];
-  QSmem &sm = *reinterpret_cast<QSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                         ~static_cast<uintptr_t>(1023));
+  // (an offset, so that the compiler still knows it for shared memory)
+  QSmem &sm = *reinterpret_cast<QSmem *>(smem_raw + (-smem_u32(smem_raw) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < kQBufs * kD; i += kQThreads) sm.nan_from[i / kD][i % kD] = ~0ull;
+  if (tid < kQBufs) sm.nan_item[tid] = -1;
   if (tid == 0) {
     prefetch_tensormap(&kv_map);
     prefetch_tensormap(&q_map);
@@ -319,6 +355,16 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
       auto ask_q = [&](const Item &x, int kk, unsigned long long wait_ns) -> bool {
         const int qb = kk % kQBufs;
         if (kk >= kQBufs && !mbar_wait(&sm.q_empty[qb], (kk / kQBufs - 1) & 1, wait_ns)) return false;
+        ItemRec rec;
+        rec.ctx = x.ctx;
+        rec.row0 = x.row0;
+        rec.t0 = x.t0;
+        rec.g = x.g;
+        rec.rows0 = x.rows0;
+        rec.rows1 = x.rows1;
+        rec.n_chunks = x.n_chunks;
+        rec.nc0 = x.nc0;
+        sm.item[qb] = rec;
         mbar_arrive_expect_tx(&sm.q_full[qb], x.halves * kOperandBytes);
         for (int h = 0; h < x.halves; ++h)
           tma_load_3d(sm.q[qb][h], &q_map, 0, x.g * kGqa, x.row0 + x.t0 + h * kQTok, &sm.q_full[qb]);
@@ -396,7 +442,8 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             c.pos = j * kChunk;
             c.n_live = it.n_keys - c.pos;
             c.flags = (j == 0 ? kFirst : 0) | (it.halves == 2 ? kTwoHalves : 0) |
-                      (c.pos + kChunk - 1 > it.ctx + it.t0 ? kDiagonal : 0) | (far ? kFarApart : 0);
+                      (c.pos + kChunk - 1 > it.ctx + it.t0 ? kDiagonal : 0) | (far ? kFarApart : 0) |
+                      (vm != kAllPages || c.n_live < kChunk ? kMasked : 0);
             c.sk = __int_as_float(top_k << 23);
             c.lv = static_cast<float>(top_v - 127);
             sm.raw_rec[st] = c;
@@ -438,6 +485,15 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           if ((issued >> st) & 1u)
             if (!mbar_wait(&sm.raw_full[st], (issued_parity >> st) & 1u, p.wait_ns))
               report(p.err, PA_DEV_TIMEOUT);
+        // no more items
+        if (ok) {
+          if (k < kQBufs || mbar_wait(&sm.q_empty[k % kQBufs], (k / kQBufs - 1) & 1, p.wait_ns)) {
+            sm.item[k % kQBufs].n_chunks = 0;
+            mbar_arrive(&sm.q_full[k % kQBufs]);
+          } else {
+            report(p.err, PA_DEV_TIMEOUT);
+          }
+        }
       }
       __syncwarp();
     } else if (warp < kMmaWarp + kHalves) {
@@ -465,20 +521,20 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         ++n_s;
         return true;
       };
-      ItemRef ref = fetch_item(sm, p, total_tiles, sorted, 0, n_items);
       for (; ok; ++k) {
-        if (ref.i < 0) break;
-        const Item it = decode_item(sm, ref);
         qb = k % kQBufs;
-        const int nch = h == 0 ? it.nc0 : it.nc1;
+        if (lane == 0) ok = mbar_wait_short(&sm.q_full[qb], (k / kQBufs) & 1, p.wait_ns) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const int n_chunks = sm.item[qb].n_chunks;
+        if (n_chunks == 0) break;
+        const int nch = h == 0 ? sm.item[qb].nc0 : sm.item[qb].nc1();
         if (lane == 0) ok = mbar_wait_short(&sm.q_ready[qb], (k / kQBufs) & 1, p.wait_ns) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (ok) ok = mma_wait_chunk(sm, gc, lane, p.wait_ns);
         if (ok && nch > 0) ok = issue_s(gc) ? 1 : 0;
-        // the next item's loads are in flight while this item's chunks run
-        ref = fetch_item(sm, p, total_tiles, sorted, k + 1, n_items);
-        for (int j = 0; j < it.n_chunks && ok; ++j, ++gc) {
-          if (j + 1 < it.n_chunks &&
+        for (int j = 0; j < n_chunks && ok; ++j, ++gc) {
+          if (j + 1 < n_chunks &&
               !mma_wait_chunk(sm, gc + 1, lane, p.wait_ns)) {
             ok = 0;
             break;
@@ -532,7 +588,6 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
     const int key0 = ct >> 2, part = ct & 3;
     const uint32_t at0 = key0 * kTileRowBytes + (((2 * part) ^ (key0 & 7)) << 4), at1 = at0 ^ 16;
     int items = 0;
-    float factor = 0.f;
     for (int gc = 0;; ++gc) {
       const int rs = gc % kRaw, ws = gc % kWide;
       ok = mbar_wait_short(&sm.raw_full[rs], (gc / kRaw) & 1, p.wait_ns);
@@ -542,56 +597,65 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
       const int qb = (items + ((rec.flags & kFirst) ? 0 : 1)) % kQBufs;   // (items counts this one already)
       if (rec.flags & kFirst) {
         // the item's Q is in, so the outputs of the item that had its buffer are out
-        ok = converters_agree(mbar_wait_short(&sm.q_full[qb], (items / kQBufs) & 1, p.wait_ns));
+        ok = mbar_wait_short(&sm.q_full[qb], (items / kQBufs) & 1, p.wait_ns);
         if (!ok) break;
-        if (ct < kD) sm.nan_from[qb][ct] = INT_MAX;
-        if (ct == 0) sm.nan_any[qb] = 0;
-        // the item's q in f16, scaled to [2^12, 2^13)
+        // thread ct turns row ct of each half into f16, scaled to [2^12, 2^13).
+        // The scores of a row that is not finite are NaN, or all -inf: its
+        // output is NaN.
         const int halves = (rec.flags & kTwoHalves) ? 2 : 1;
-        uint32_t top = 0;
-        for (int h = 0; h < halves; ++h)
-          top = max(top, q_row_top(sm.q[qb][h] + ct * kTileRowBytes, ct));
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) sm.q_top[warp & 3] = top;
-        asm volatile("bar.sync 1, %0;" ::"n"(kConvThreads) : "memory");
-        top = max(max(sm.q_top[0], sm.q_top[1]), max(sm.q_top[2], sm.q_top[3]));
-        const int f = min(266 - static_cast<int>(top >> 7), 253);   // exponent field of the scale
-        for (int h = 0; h < halves; ++h)
-          q_row_to_f16(sm.q[qb][h] + ct * kTileRowBytes, ct, __int_as_float(f << 23));
-        factor = p.qscale * __int_as_float((254 - f) << 23);
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {
+          unsigned char *row = sm.q[qb][h] + ct * kTileRowBytes;
+          const int e = static_cast<int>(q_row_top(row, ct) >> 7);
+          q_row_to_f16(row, ct, __int_as_float(q_scale_field(e) << 23));
+          sm.q_exp[qb][h][ct] = static_cast<uint8_t>(e);
+        }
         fence_proxy_async_smem();       // the tensor core reads q through the async proxy
         mbar_arrive(&sm.q_ready[qb]);
         ++items;
       }
       ok = mbar_wait_short(&sm.kv_empty[ws], ((gc / kWide) & 1) ^ 1, p.wait_ns);
       if (!ok) break;
+      const uint32_t mul_step = kConvThreads / 4 / BT * 8;
+      uint32_t src = smem_u32(sm.raw[rs][0]) + 16 * ct, mul_at = smem_u32(&sm.raw_mul[rs][key0 / BT]);
+      uint32_t dst = smem_u32(sm.k[ws]) + at0;
+      const uint32_t flip = at1 - at0, to_v = smem_u32(sm.v[ws]) - smem_u32(sm.k[ws]);
+      int key = key0;
 #pragma unroll 1
       for (int i = 0; i < kChunk * 4 / kConvThreads; ++i) {
-        const int key = key0 + i * (kConvThreads / 4);
-        const uint2 mul = sm.raw_mul[rs][key / BT];
-        const uint32_t row = i * (kConvThreads / 4 * kTileRowBytes);
-        const uint4 kr = reinterpret_cast<const uint4 *>(sm.raw[rs][0])[ct + i * kConvThreads];
-        *reinterpret_cast<uint4 *>(sm.k[ws] + row + at0) = widen8(kr.x, kr.y, mul.x);
-        *reinterpret_cast<uint4 *>(sm.k[ws] + row + at1) = widen8(kr.z, kr.w, mul.x);
-        uint4 vr = reinterpret_cast<const uint4 *>(sm.raw[rs][1])[ct + i * kConvThreads];
-        if (key >= rec.n_live || !((rec.mask >> (key / BT)) & 1)) vr = make_uint4(0, 0, 0, 0);
-        // a NaN value would reach the rows before it too (P = 0 times NaN)
-        if ((rec.flags & kDiagonal) &&
-            (nan_bytes(vr.x) | nan_bytes(vr.y) | nan_bytes(vr.z) | nan_bytes(vr.w)) != 0) {
-          int *from = sm.nan_from[qb] + 16 * part;
-          vr.x = without_nan(vr.x, 0, rec.pos + key, from);
-          vr.y = without_nan(vr.y, 4, rec.pos + key, from);
-          vr.z = without_nan(vr.z, 8, rec.pos + key, from);
-          vr.w = without_nan(vr.w, 12, rec.pos + key, from);
-          sm.nan_any[qb] = 1;
+        const uint2 mul = lds8(mul_at);
+        const uint4 kr = lds16(src);
+        uint4 vr = lds16(src + kChunk * kQ8HeadBytes);
+        uint4 w0 = widen8(kr.x, kr.y), w1 = widen8(kr.z, kr.w);
+        if (mul.x != 0x3c003c00u) { w0 = mul8(w0, mul.x); w1 = mul8(w1, mul.x); }
+        sts16(dst, w0);
+        sts16(dst + flip, w1);
+        if (rec.flags & (kMasked | kDiagonal)) {
+                  if (key >= rec.n_live || !((rec.mask >> (key / BT)) & 1)) vr = make_uint4(0, 0, 0, 0);
+          // a NaN value would reach the rows before it too (P = 0 times NaN)
+          if ((rec.flags & kDiagonal) &&
+              (nan_bytes(vr.x) | nan_bytes(vr.y) | nan_bytes(vr.z) | nan_bytes(vr.w)) != 0) {
+            unsigned long long *from = sm.nan_from[qb] + 16 * part;
+            vr.x = without_nan(vr.x, 0, items - 1, rec.pos + key, from);
+            vr.y = without_nan(vr.y, 4, items - 1, rec.pos + key, from);
+            vr.z = without_nan(vr.z, 8, items - 1, rec.pos + key, from);
+            vr.w = without_nan(vr.w, 12, items - 1, rec.pos + key, from);
+            sm.nan_item[qb] = items - 1;
+          }
         }
-        *reinterpret_cast<uint4 *>(sm.v[ws] + row + at0) = widen8(vr.x, vr.y, mul.y);
-        *reinterpret_cast<uint4 *>(sm.v[ws] + row + at1) = widen8(vr.z, vr.w, mul.y);
+        w0 = widen8(vr.x, vr.y), w1 = widen8(vr.z, vr.w);
+        if (mul.y != 0x3c003c00u) { w0 = mul8(w0, mul.y); w1 = mul8(w1, mul.y); }
+        sts16(dst + to_v, w0);
+        sts16(dst + to_v + flip, w1);
+        src += 16 * kConvThreads;
+        mul_at += mul_step;
+        dst += kConvThreads / 4 * kTileRowBytes;
+        key += kConvThreads / 4;
       }
       if (ct < kPagesPerChunk) sm.lv[ws][ct] = sm.raw_lv[rs][ct];
       if (ct == 0) {
         sm.pmask[ws] = rec.mask;
-        sm.scale[ws] = make_float4(fmaxf(factor * rec.sk, kTiny), rec.lv, p_exp2(-rec.lv),
+        sm.scale[ws] = make_float4(rec.sk, rec.lv, p_exp2(-rec.lv),
                                    (rec.flags & kFarApart) ? 1.f : 0.f);
       }
       mbar_arrive(&sm.raw_empty[rs]);
@@ -630,22 +694,20 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         pend_qb = -1;
       }
     };
-    ItemRef ref = fetch_item(sm, p, total_tiles, sorted, 0, n_items);
-    for (int k = 0; ok; ++k) {
-      if (ref.i < 0) break;
-      const Item it = decode_item(sm, ref);
-      // the next item's loads are in flight while this item's chunks run
-      ref = fetch_item(sm, p, total_tiles, sorted, k + 1, n_items);
-      const int rows = h == 0 ? it.rows0 : it.rows1;
-      const int nch = h == 0 ? it.nc0 : it.nc1;
+    for (int k = 0;; ++k) {
       const int qb = k % kQBufs;
+      ok = mbar_wait_short(&sm.q_full[qb], (k / kQBufs) & 1, p.wait_ns);
+      if (!ok) break;
+      const ItemRec it = sm.item[qb];
+      if (it.n_chunks == 0) break;
+      const int rows = h == 0 ? it.rows0 : it.rows1;
+      const int nch = h == 0 ? it.nc0 : it.nc1();
       if (nch == 0) {
-        // nothing staged: release the Q buffer, once it holds this item's Q
-        // (an earlier arrival would count for the item before last)
+        // nothing staged: release the Q buffer (it holds this item's Q: an
+        // earlier arrival would count for the item before last)
         if (r == 0) {
           release_stored();
-          ok = mbar_wait_short(&sm.q_full[qb], (k / kQBufs) & 1, p.wait_ns);
-          if (ok) mbar_arrive(&sm.q_empty[qb]);
+          mbar_arrive(&sm.q_empty[qb]);
         }
         gc += it.n_chunks;
         continue;
@@ -653,13 +715,18 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
       const int first_pos = it.ctx + it.t0 + h * kQTok;   // the half's first query position
       const int last_pos = first_pos + rows - 1;
       const int qpos = min(first_pos + tok, last_pos);
-      float m = p_neg_inf(), l = 0.f;
+      float m = p_neg_inf(), l = 0.f, factor = 0.f;
       for (int j = 0; j < nch; ++j) {
         const int st = (gc + j) % kWide;
         if (!mbar_wait_short(&sm.s_full[h], n_s & 1, p.wait_ns) ||
             !mbar_wait_short(&sm.kv_full[st], ((gc + j) / kWide) & 1, p.wait_ns)) {
           ok = false;
           break;
+        }
+        if (j == 0) {   // (q was converted before the item's first chunk was widened)
+          const int e = sm.q_exp[qb][h][r];
+          factor = e < 255 ? p.qscale * __int_as_float((254 - q_scale_field(e)) << 23)
+                           : __int_as_float(0x7fc00000);
         }
         ++n_s;
         tc::fence_after_sync();
@@ -668,8 +735,9 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         // every key of the chunk is visible to every row of the half and was loaded
         const bool full = pm == static_cast<int>(kAllPages) && kbase + kChunk - 1 <= first_pos;
         const int lim = qpos - kbase;           // keys c <= lim are at or before the row
-        const float4 sc = sm.scale[st];         // f sK, log2 sV, 1 / sV, V's pages far apart
-        const float2 f2 = make_float2(sc.x, sc.x);
+        const float4 sc = sm.scale[st];         // sK, log2 sV, 1 / sV, V's pages far apart
+        const float fk = fmaxf(factor * sc.x, kTiny);
+        const float2 f2 = make_float2(fk, fk);
         bool pv_done = j == 0;                  // PV_{j-1} complete: O stable, P columns read
         auto wait_pv = [&]() -> bool {
           if (pv_done) return true;
@@ -729,7 +797,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
               mx8[q] = fmax3(mx8[q], __uint_as_float(v[c + q]), __uint_as_float(v[c + 8 + q]));
           const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                  fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-          if (!move_to(fmaf(mx, sc.x, sc.y))) {
+          if (!move_to(fmaf(mx, fk, sc.y))) {
             ok = false;
             break;
           }
@@ -773,7 +841,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             float mx = x[0];
 #pragma unroll
             for (int c = 1; c < 8; ++c) mx = fmaxf(mx, x[c]);
-            mc = fmaxf(mc, fmaf(mx, sc.x, sm.lv[st][c0 / BT]));
+            mc = fmaxf(mc, fmaf(mx, fk, sm.lv[st][c0 / BT]));
           }
           if (!move_to(mc) || !wait_pv()) {
             ok = false;
@@ -788,8 +856,8 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             uint32_t w[4];
 #pragma unroll
             for (int c = 0; c < 8; c += 2) {
-              const float e0 = p_exp2(fmaf(x[c], sc.x, lv - base));
-              const float e1 = p_exp2(fmaf(x[c + 1], sc.x, lv - base));
+              const float e0 = p_exp2(fmaf(x[c], fk, lv - base));
+              const float e1 = p_exp2(fmaf(x[c + 1], fk, lv - base));
               sum += e0 + e1;
               w[c >> 1] = pack_f16(e0, e1);
             }
@@ -818,7 +886,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       mbar_arrive(&sm.o_free[h]);   // the next item's first PV may clear O
-      const float inv = (l > 0.f) ? 1.f / l : 0.f;
+      const float inv = factor != factor ? factor : (l > 0.f) ? 1.f / l : 0.f;
       auto row_chunk = [&](int e) {
         const float *f = reinterpret_cast<const float *>(&ov[8 * e]);
         return make_uint4(float2_to_bf16x2(f[0] * inv, f[1] * inv),
@@ -835,10 +903,10 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
 #pragma unroll
         for (int e = 0; e < kD / 8; ++e)
           *reinterpret_cast<uint4 *>(stg + ((e ^ (r & 7)) << 4)) = row_chunk(e);
-        if (sm.nan_any[qb])   // NaN values that the row sees among the item's last keys
+        if (sm.nan_item[qb] == k)   // NaN values that the row sees among the item's last keys
 #pragma unroll 1
           for (int d = 0; d < kD; ++d)
-            if (sm.nan_from[qb][d] <= qpos)
+            if (sees_nan(sm.nan_from[qb][d], k, qpos))
               *reinterpret_cast<uint16_t *>(stg + (((d >> 3) ^ (r & 7)) << 4) + 2 * (d & 7)) = 0x7fc0;
         fence_proxy_async_smem();
         mbar_arrive(&sm.staged[h]);
@@ -859,10 +927,10 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
                        it.g * kGqa + hh) * kD);
 #pragma unroll
           for (int e = 0; e < kD / 8; ++e) dst[e] = row_chunk(e);
-          if (sm.nan_any[qb])
+          if (sm.nan_item[qb] == k)
 #pragma unroll 1
             for (int d = 0; d < kD; ++d)
-              if (sm.nan_from[qb][d] <= qpos) reinterpret_cast<uint16_t *>(dst)[d] = 0x7fc0;
+              if (sees_nan(sm.nan_from[qb][d], k, qpos)) reinterpret_cast<uint16_t *>(dst)[d] = 0x7fc0;
         }
         // the buffer's NaN record is read by every row before it is released
         mbar_arrive(&sm.staged[h]);
@@ -873,6 +941,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         }
         ++n_staged;
       }
+      if (!ok) break;
       gc += it.n_chunks;
     }
     if (!ok) report(p.err, PA_DEV_TIMEOUT);

@@ -521,6 +521,23 @@ def test_prefill_nan_key_and_value():
     assert np.array_equal(np.isnan(got), bad)
 
 
+@pytest.mark.parametrize("bad", [0x7F80, 0xFF80, 0x7FC0])
+def test_prefill_q_row_not_finite(bad):
+    """An infinity or NaN in a row of q makes that row's output NaN and changes no other row."""
+    rng, pool, scales, table, _ = _cache(8, [200], 16)
+    q = wl.normal_bf16(rng, (150, N_Q, D))
+    want, _ = _prefill(q, _cu([150]), pool, scales, table, [50])
+    q = q.copy()
+    q[40, 9, 3] = bad
+    q[100, 31, 63] = bad
+    got, err = _prefill(q, _cu([150]), pool, scales, table, [50])
+    assert err == 0
+    rows = np.zeros((150, N_Q), bool)
+    rows[40, 9] = rows[100, 31] = True
+    assert np.isnan(got[rows]).all()
+    assert np.array_equal(got[~rows], want[~rows])
+
+
 def test_prefill_wait_that_runs_out():
     """A chunk announced but never copied (the library's test hook): the call
     reports the time-out, and the next one is right."""
