@@ -1,22 +1,28 @@
 """Builds the in-tree CUDA library ``_build/libpagedkv.so`` for sm_103a.
 
 Plain nvcc, no cmake: each ``csrc/*.cu`` compiles in parallel to an object
-file, then one ``nvcc -shared`` link.  A rebuild happens only when a source
-or header is newer than the library.
+file, then one ``nvcc -shared`` link.  Beside it ``_build/_pa_torch.so``, the
+extension module that hands torch tensors to the library (``csrc/pa_torch.cpp``,
+host code, g++).  A rebuild happens only when a source or header is newer than
+what was built.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpagedkv.so")
+TORCH_SRC = os.path.join(CSRC, "pa_torch.cpp")
+TORCH_LIB = os.path.join(BUILD, "_pa_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
               "--expt-relaxed-constexpr"]
@@ -31,16 +37,31 @@ def _nvcc() -> str:
 
 def _inputs():
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
+    deps = srcs + [TORCH_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
         + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
     return srcs, deps
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(TORCH_LIB):
         return False
     _, deps = _inputs()
-    return os.path.getmtime(LIB) >= max(os.path.getmtime(d) for d in deps)
+    built = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
+    return built >= max(os.path.getmtime(d) for d in deps)
+
+
+def _build_torch_module() -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(torch, "include"),
+           "-I" + os.path.join(cuda, "include"), TORCH_SRC, "-o", tmp,
+           "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {TORCH_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
@@ -58,8 +79,10 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        module = ex.submit(_build_torch_module)
         results = list(ex.map(compile_one, srcs))
+        module.result()
     if verbose:
         for _, log in results:
             print(log)

@@ -635,3 +635,144 @@ def test_prompts_then_decode_steps_then_free(page):
     _, _, bt, count, err = st.host()
     assert err == 0 and count == blocks and np.all(bt == -1)
     assert np.array_equal(np.sort(st.fl.cpu().numpy()), np.arange(blocks))
+
+
+# ------------------------------------------------------------ ways to call them
+def test_default_explicit_and_side_stream_agree():
+    """The current stream by default, a stream given, a side stream made current:
+    the same bits from each of the four calls."""
+    import torch
+    pk = _pk()
+    lens = [40, 0, 129, 7]
+    k, v, q, cu, pool, scales, table, fl, fc = _append_case(91, lens, [3, 1, 20, 0], 16)
+    side = torch.cuda.Stream()
+
+    def run(stream, current):
+        st = _State(pool, scales, table, fl, fc)
+        n, ctx = len(lens), dev_i32(lens)
+        kd, vd, qd, cud = dev_bf16(k), dev_bf16(v), dev_bf16(q), dev_i32(cu)
+        turned, out, dec = torch.zeros_like(qd), torch.zeros_like(qd), torch.zeros_like(qd[:n])
+        ws = pk.decode_workspace_q8(n, table.shape[2])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(current):
+            pk.pa_prefill_append_rope_q8(kd, vd, qd, cud, st.kv, st.sc, st.bt, ctx, 1, st.fl, st.fc, st.err,
+                                         stream=stream, q_out=turned)
+            pk.pa_prefill_attention_q8(out, turned, cud, st.kv, st.sc, st.bt, ctx, 1, 0.125, st.err, stream=stream)
+            after = ctx + (cud[1:] - cud[:-1]) if stream is None else dev_i32(np.add(lens, np.diff(cu)))
+            pk.pa_kv_append_rope_q8(kd[:n], vd[:n], qd[:n], st.kv, st.sc, st.bt, after, 1, st.fl, st.fc, st.err,
+                                    stream=stream)
+            pk.pa_decode_attention_q8(dec, qd[:n], st.kv, st.sc, st.bt, dev_i32(np.add(lens, np.diff(cu)) + 1), 1,
+                                      0.125, ws, st.err, stream=stream)
+        torch.cuda.synchronize()
+        return [turned, out, dec, qd, *map(torch.from_numpy, st.host()[:3]), *st.host()[3:]]
+
+    main = torch.cuda.current_stream()
+    want = run(None, main)
+    assert want[-1] == 0
+    for got in (run(main, main), run(None, side)):
+        for a, b in zip(got, want):
+            assert torch.equal(a, b) if isinstance(a, torch.Tensor) else a == b
+
+
+def test_two_graphs_share_a_workspace():
+    """Graphs of different batches captured over one workspace, replayed one after
+    the other in either order, with an eager call between."""
+    import torch
+    pk = _pk()
+    batches, ws = [], None
+    for seed, lens in ((71, [3000, 20, 900]), (72, [64] * 40)):
+        rng, pool, scales, table, _ = _cache(seed, lens, 16)
+        kv, sc = _dev_pool(pool, scales)
+        q, err = dev_bf16(wl.normal_bf16(rng, (len(lens), N_Q, D))), dev_i32([0])
+        if ws is None:
+            ws = pk.decode_workspace_q8(40, 200)
+        args = (q, kv, sc, dev_i32(table), dev_i32(lens), 0, 0.125, ws, err)
+        want, out = torch.empty_like(q), torch.empty_like(q)
+        pk.pa_decode_attention_q8(want, *args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pk.pa_decode_attention_q8(out, *args)
+        batches.append((g, out, want, args))
+    for order in ((0, 1), (1, 0), (0, 0, 1)):
+        for i in order:
+            g, out, want, args = batches[i]
+            out.fill_(float("nan"))
+            g.replay()
+            other = torch.empty_like(batches[1 - i][1])
+            pk.pa_decode_attention_q8(other, *batches[1 - i][3])
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(other, batches[1 - i][2])
+
+
+def test_prefill_graph_replayed_with_other_lengths():
+    """Captured once; replayed with other contexts, splits and inputs: a direct call's bits."""
+    import torch
+    pk = _pk()
+    rng, pool, scales, table, _ = _cache(61, [500, 300, 200], 16)
+    kv, sc = _dev_pool(pool, scales)
+    rows = 180
+    q, out = (torch.zeros((rows, N_Q, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cu, ctx, err = dev_i32(_cu([100, 50, 30])), dev_i32([400, 0, 0]), dev_i32([0])
+    args = (q, cu, kv, sc, dev_i32(table), ctx, 0, 0.125, err)
+    g = torch.cuda.CUDAGraph()
+    pk.pa_prefill_attention_q8(out, *args)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        pk.pa_prefill_attention_q8(out, *args)
+    for lens, c in (([100, 50, 30], [400, 0, 0]), ([0, 179, 1], [0, 121, 199]), ([64, 0, 116], [1, 5, 0])):
+        cu.copy_(dev_i32(_cu(lens))), ctx.copy_(dev_i32(c))
+        q.copy_(dev_bf16(wl.normal_bf16(rng, (rows, N_Q, D))))
+        direct = torch.full_like(q, float("nan"))
+        pk.pa_prefill_attention_q8(direct, *args)
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, direct) and bool(torch.isfinite(direct).all())
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("tiles", [2047, 2048, 2049])
+def test_prefill_as_many_tiles_as_are_sorted(tiles):
+    """One more tile than the work order holds, and up to it: sequences of one
+    token, and one of as many tiles as are left."""
+    lens = [1] * 1900 + [64 * (tiles - 1900) - 63]
+    page = 16
+    ctx = [3] * 1900 + [0]
+    rng, pool, scales, table, _ = _cache(tiles, [c + n for c, n in zip(ctx, lens)], page, poison=False)
+    q = wl.normal_bf16(rng, (sum(lens), N_Q, D))
+    got, err = _prefill(q, _cu(lens), pool, scales, table, ctx)
+    assert err == 0 and np.all(np.isfinite(got))
+    # the single tokens, and the long one's first and last rows (as decode rows)
+    n = 1900
+    rows = list(range(n)) + [n, n + 63, n + 64, sum(lens) - 1]
+    t = np.concatenate([table[:n], np.repeat(table[n:], 4, 0)])
+    seen = [4] * n + [r - n + 1 for r in rows[n:]]
+    ref, _ = oracle.decode_attention(q[rows], q8.pool_bf16(pool, scales), t, seen, 0, block_tokens=page)
+    _assert_close(got[rows], ref, q[rows], pool, scales, max(seen), 0.125, 2.0 ** -12)
+
+
+@pytest.mark.parametrize("page", PAGES)
+def test_prefill_append_of_many_short_chunks(page):
+    """More sequences than the CTA has threads, most of a token or three, some
+    empty, some refused (past the table's end, or a negative context)."""
+    rng = np.random.default_rng(page)
+    n = 1100
+    lens = rng.integers(0, 4, n)
+    lens[[5, 700]] = [2 * page + 1, page]
+    ctx = rng.integers(0, 3 * page, n)
+    k, v, q, cu, pool, scales, table, fl, fc = _append_case(40 + page, ctx.tolist(), lens.tolist(), page, layers=1,
+                                                            layer=0)
+    ctx[[9, 900]] = [-1, table.shape[2] * page]
+    ref = q8.append(k, v, q, cu, pool, scales, table, ctx.tolist(), 0, fl, fc)
+    st = _State(pool, scales, table, fl, fc)
+    qd = dev_bf16(q)
+    _pk().pa_prefill_append_rope_q8(dev_bf16(k), dev_bf16(v), qd, dev_i32(cu), st.kv, st.sc, st.bt, dev_i32(ctx), 0,
+                                    st.fl, st.fc, st.err)
+    _compare(st, ref)
+    # the rotation is off by at most 2^-22 (|a| + |b|), below 3e-6 for |q| < 6: one
+    # step of the result, or, where the two products cancel and steps are smaller
+    # than that, less than 1.5e-5
+    got = host_bits(qd)
+    assert np.all((ulp_diff(got, ref[0]) <= 1) |
+                  (np.abs(oracle.bf16_to_f64(got) - oracle.bf16_to_f64(ref[0])) <= 1.5e-5))

@@ -163,6 +163,10 @@ def test_workspace_size():
     assert 0 < pk.pa_decode_workspace_size_q8(1, 1) <= pk.pa_decode_workspace_size_q8(256, 512, 32)
 
 
+def test_prompt_append_refuses_more_sequences_than_its_grid_holds():
+    assert _call("pa_prefill_append_rope_q8", n=(1 << 29) + 1) == -2
+
+
 def test_binding_refuses_before_the_library():
     """Tensors off the device, of other types or shapes do not reach the library."""
     import paged_kv_cache_205_gb300 as pk
