@@ -7,12 +7,13 @@
 //                            k and v to the page's scale; where the new token
 //                            needs a larger scale than the page has, the
 //                            page's earlier tokens are brought to it.
-//   prefill_store_q8_kernel  one CTA per page that the call's rows touch, half
-//                            its warps on k and v, half on q; a page's values
-//                            stay in registers between the maximum that sets
-//                            the scale and the rounding.
+//   prefill_store_q8_kernel  one CTA per page that the call's rows touch (its
+//                            values stay in registers between the maximum that
+//                            sets the scale and the rounding), and one per 8
+//                            or 16 rows of q.
 // Both are bound by memory (large) or latency (small): a row costs 2 KiB of k
 // and v read, 1 KiB of bytes written, 4 KiB of q read and 4 KiB written.
+#include <algorithm>
 #include <cuda_fp16.h>
 
 #include "pa_append_shared.cuh"
@@ -21,10 +22,81 @@
 namespace pa {
 namespace {
 
+// What the rotations need, worked out on the host and passed by value: cos and
+// sin of 2 pi i / 64, and the pairs' frequencies as fp32 head and rest.
+constexpr int kAngles = 64;
+struct AngleTable {
+  float2 e[kAngles];
+  float2 f[kD / 2];
+};
+
+AngleTable angle_table(const RopeFreqs &freqs) {
+  AngleTable t;
+  for (int i = 0; i < kAngles; ++i) {
+    const double a = i * (6.283185307179586476925 / kAngles);
+    t.e[i] = make_float2(static_cast<float>(std::cos(a)), static_cast<float>(std::sin(a)));
+  }
+  for (int d = 0; d < kD / 2; ++d) {
+    t.f[d].x = static_cast<float>(freqs.f[d]);
+    t.f[d].y = static_cast<float>(freqs.f[d] - t.f[d].x);
+  }
+  return t;
+}
+
 struct Q8Out {
   uint16_t *q_out;   // where rotated q goes (may be q itself)
   float *scales;
+  AngleTable table;
 };
+
+// The angle pos * f less at * 2 pi / 64, as fp32 head and rest, |.| <= pi / 64.
+struct BaseAngle {
+  float r, rest;
+  int at;
+};
+
+// Formed and reduced in fp64; the multiple of 2 pi / 64 is taken off in two fused
+// multiply-adds, head first (W. J. Cody, W. Waite, "Software Manual for the
+// Elementary Functions", 1980).
+__device__ __forceinline__ BaseAngle base_angle(int pos, double f) {
+  constexpr double kStepHi = 6.283185307179586232 / kAngles;
+  constexpr double kStepLo = 2.4492935982947064e-16 / kAngles;
+  constexpr double kInteger = 6755399441055744.0;   // 1.5 * 2^52: adding it rounds to an integer
+  const double a = static_cast<double>(pos) * f;
+  const double t = fma(a, 0.15915494309189533577 * kAngles, kInteger);
+  const double k = t - kInteger;
+  const double r = fma(-k, kStepLo, fma(-k, kStepHi, a));
+  BaseAngle b;
+  b.r = static_cast<float>(r);
+  b.rest = static_cast<float>(r - static_cast<double>(b.r));
+  b.at = __double2loint(t) & (kAngles - 1);
+  return b;
+}
+
+// (cos, sin) of the angle of `step` (< 32) positions after b's, within 2^-23.
+// Everything in fp32, so that fp64, at a sixteenth of a warp a cycle and SM, works
+// out one row's angles of a CTA and not all rows': step * f and the sum with the
+// base keep their rounding errors, the multiple k <= 327 of 2 pi / 64 is taken
+// off with an 8-bit head (k times it is exact) and a rest, the table holds the
+// grid point, and the addition theorem adds what is left, |r| <= pi / 64 + 2^-20,
+// whose sine and 1 - cosine are short Taylor sums (r^7 / 5040 < 2^-42).
+__device__ __forceinline__ float2 angle_cos_sin(const BaseAngle &b, int step, float2 f,
+                                                const float2 *table) {
+  constexpr float kStepHead = 0.09814453125f;                            // 2 pi / 64 to 8 bits
+  constexpr float kStepRest = static_cast<float>(0.098174770424681038701 - 0.09814453125);
+  const float t = static_cast<float>(step);
+  const float p = t * f.x, pe = fmaf(t, f.x, -p);
+  const float s = b.r + p, v = s - b.r;
+  const float se = (b.r - (s - v)) + (p - v);                            // s + se = b.r + p
+  const float k = rintf(s * 10.185916357881302f);
+  const float low = se + fmaf(t, f.y, b.rest + pe);
+  const float r = fmaf(-k, kStepHead, s) + fmaf(-k, kStepRest, low);
+  const float2 e = table[(b.at + static_cast<int>(k)) & (kAngles - 1)];
+  const float r2 = r * r;
+  const float cm1 = r2 * fmaf(r2, 1.f / 24, -0.5f);                      // cos r - 1
+  const float sn = fmaf(r * r2, fmaf(r2, 1.f / 120, -1.f / 6), r);       // sin r
+  return make_float2(e.x + fmaf(e.x, cm1, -e.y * sn), e.y + fmaf(e.y, cm1, e.x * sn));
+}
 
 // (lo, hi) of 4 consecutive pairs of one head row: bf16 words of dims
 // 4j..4j+3 and 32+4j..32+4j+3.
@@ -69,7 +141,8 @@ __global__ void __launch_bounds__(kStoreQ8Threads) append_store_q8_kernel(Append
   } else if (p.q) {
     x = load_part(p.q + (static_cast<size_t>(s) * kHq + head - 2 * kHkv) * kD, j);
   }
-  if (tid < kD / 2) cs[tid] = rope_cos_sin(pos, p.freqs.f[tid]);
+  if (tid < kD / 2)
+    cs[tid] = angle_cos_sin(base_angle(pos, p.freqs.f[tid]), 0, make_float2(0.f, 0.f), o.table.e);
   // the largest magnitude of the head's 64 values, before the rotation
   uint32_t top = q8_top(x.hi.y, q8_top(x.hi.x, q8_top(x.lo.y, q8_top(x.lo.x, 0u))));
 #pragma unroll
@@ -151,10 +224,8 @@ struct __align__(16) RowAngles {
 // The pairs (lo, hi) of one bf16 word each, rotated by (x, y) and (z, w).
 __device__ __forceinline__ void rotate2(uint32_t *lo, uint32_t *hi, float4 cs) {
   const float2 a = bf16x2_to_float2(*lo), b = bf16x2_to_float2(*hi);
-  *lo = float_to_bf16_bits(fmaf(a.x, cs.x, -b.x * cs.y)) |
-        (float_to_bf16_bits(fmaf(a.y, cs.z, -b.y * cs.w)) << 16);
-  *hi = float_to_bf16_bits(fmaf(b.x, cs.x, a.x * cs.y)) |
-        (float_to_bf16_bits(fmaf(b.y, cs.z, a.y * cs.w)) << 16);
+  *lo = float2_to_bf16x2(fmaf(a.x, cs.x, -b.x * cs.y), fmaf(a.y, cs.z, -b.y * cs.w));
+  *hi = float2_to_bf16x2(fmaf(b.x, cs.x, a.x * cs.y), fmaf(b.y, cs.z, a.y * cs.w));
 }
 
 // 16 bytes (8 bf16) of one half of a head row, rotated against the other half.
@@ -169,40 +240,127 @@ __device__ __forceinline__ uint32_t q8_top4(uint4 w, uint32_t top) {
   return q8_top(w.w, q8_top(w.z, q8_top(w.y, q8_top(w.x, top))));
 }
 
-// A CTA takes the rows of one call that fall into one page.  Sequence s owns
+// The largest magnitudes (bf16 patterns, infinities and NaN among them) of the
+// even and the odd elements of w, and of `top`.
+__device__ __forceinline__ uint32_t any_top4(uint4 w, uint32_t top) {
+  constexpr uint32_t kMag = 0x7fff7fffu;
+  return __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & kMag, w.y & kMag), __vmaxu2(w.z & kMag, w.w & kMag)));
+}
+
+// Eight bf16 times `inv` to eight e4m3; plain: none of them is infinite.
+__device__ __forceinline__ uint2 quantise8(uint4 w, float inv, bool plain) {
+  if (plain) {
+    uint2 r;
+    float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+    r.x = e4m3x2_plain(a.x * inv, a.y * inv) | (e4m3x2_plain(b.x * inv, b.y * inv) << 16);
+    a = bf16x2_to_float2(w.z);
+    b = bf16x2_to_float2(w.w);
+    r.y = e4m3x2_plain(a.x * inv, a.y * inv) | (e4m3x2_plain(b.x * inv, b.y * inv) << 16);
+    return r;
+  }
+  return make_uint2(bf16x4_to_e4m3x4(w.x, w.y, inv), bf16x4_to_e4m3x4(w.z, w.w, inv));
+}
+
+// A page CTA takes the rows of one call that fall into one page.  Sequence s owns
 // CTAs cu_tokens[s] / BT + 2 s and up: n rows touch at most n / BT + 2 pages, so
 // the ranges do not meet, and total_tokens / BT + 2 num_seqs CTAs hold them all.
-// Half its warps take k and v (two rows of each a warp, held in registers
-// between the maximum that sets the scale and the rounding), half q; the angles
-// (fp64, a tenth of the instructions but a quarter of the time on that pipe) are
-// worked out once for both.  64 registers let two CTAs of 512 threads, 128 KiB of
-// loads, be on the way per SM.  8 x 2048 tokens take 36.5 us, 184 MB at 5.1 TB/s
-// (a CTA per window of rows with every warp on k, v and q in turn, 104 registers
-// and one CTA an SM: 53 us); 31 tokens 8.9 us, the allocation and the loads one
-// after another.
+// The other CTAs take kQRows packed rows of q each: one per SM (`lead`) before the
+// page CTAs, which meanwhile wait for the pages that the allocation kernel hands
+// out, and the rest after them.  CTAs of 64 registers, four (256 threads) an SM.
+// Bound by memory and by each CTA's chain of load, angle, maximum, table entry and
+// store: 8 x 2048 tokens 32.9 us, 184 MB at 5.6 TB/s (no q CTA first 34.7, 304
+// first 33.2; q in the page CTAs, every row's angles in fp64 36.5; a CTA per window
+// of rows with every warp on k, v and q in turn 53), 31 tokens 6.4 us.
 template <int BT>
 struct StoreGeom {
-  static constexpr int kThreads = 32 * BT;
-  static constexpr int kRole = kThreads / 2;         // threads for k and v, threads for q
-  static constexpr int kPassRows = kRole / 32;       // 4 threads per kv head and row
-  static constexpr int kPasses = 2;
-  static constexpr int kQBatch = 4;                  // parts of q rows a thread holds
-  static constexpr int kQBatches = 2;
-  static_assert(kPassRows * kPasses == BT && kRole * kQBatch * kQBatches == BT * kHq * 4, "");
+  static constexpr int kThreads = BT == 32 ? 512 : 256;
+  static constexpr int kPassRows = kThreads / 32;    // rows of k and v a pass takes: 4 threads per kv head
+  static constexpr int kPasses = BT / kPassRows;     // 1, 2, 2
+  static constexpr int kQRows = kThreads / 32;
+  static constexpr int kQParts = 4;                  // 16-byte parts (and their partners) a thread holds
+  static constexpr int kRows = BT > kQRows ? BT : kQRows;
+  static_assert(kPassRows * kPasses == BT && kThreads * kQParts == kQRows * kHq * 4, "");
 };
+
+// The packed rows [r0, r0 + kQRows) of q, rotated.
+template <int BT>
+__device__ __forceinline__ void rotate_q_rows(const PrefillAppendParams &p, const Q8Out &o, int r0,
+                                              RowAngles *cs, int *row_pos, int *row_run,
+                                              BaseAngle (*base)[kD / 2], const AngleTable &table) {
+  using G = StoreGeom<BT>;
+  const int tid = threadIdx.x, c = tid & 3;
+  uint4 lo[G::kQParts], hi[G::kQParts];
+  auto at = [&](int i) -> size_t {   // part i of the thread: row, head, part c
+    const int item = tid + i * G::kThreads;
+    return (static_cast<size_t>(r0 + (item >> 7)) * kHq + ((item >> 2) & 31)) * kD + 8 * c;
+  };
+  auto row_of = [&](int i) { return (tid + i * G::kThreads) >> 7; };
+#pragma unroll
+  for (int i = 0; i < G::kQParts; ++i) {
+    lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+    if (r0 + row_of(i) < p.total_tokens) {
+      lo[i] = *reinterpret_cast<const uint4 *>(p.q + at(i));
+      hi[i] = *reinterpret_cast<const uint4 *>(p.q + at(i) + kD / 2);
+    }
+  }
+  if (tid < G::kQRows) row_pos[tid] = -1;   // rows of refused chunks stay as they are
+  __syncthreads();
+  for (int s = tid; s < p.num_seqs; s += G::kThreads) {
+    const int a = p.cu_tokens[s], b = p.cu_tokens[s + 1];
+    if (a >= r0 + G::kQRows || b <= r0) continue;
+    int ctx, n;
+    if (!chunk_fits<BT>(p, s, &ctx, &n)) continue;
+    const int run = max(a, r0);
+    for (int r = run; r < min(b, r0 + G::kQRows); ++r) {
+      row_pos[r - r0] = ctx + (r - a);
+      row_run[r - r0] = run - r0;
+    }
+  }
+  __syncthreads();
+  for (int x = tid; x < G::kQRows * (kD / 2); x += G::kThreads) {
+    const int t = x / (kD / 2), d = x % (kD / 2);
+    if (row_pos[t] >= 0 && row_run[t] == t) base[t][d] = base_angle(row_pos[t], p.freqs.f[d]);
+  }
+  __syncthreads();
+  for (int x = tid; x < G::kQRows * (kD / 2); x += G::kThreads) {
+    const int t = x / (kD / 2), d = x % (kD / 2);
+    if (row_pos[t] < 0) continue;
+    cs[t].set(d, angle_cos_sin(base[row_run[t]][d], t - row_run[t], table.f[d], table.e));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < G::kQParts; ++i) {
+    if (row_pos[row_of(i)] < 0) continue;
+    rotate8(&lo[i], &hi[i], cs[row_of(i)], c);
+    *reinterpret_cast<uint4 *>(o.q_out + at(i)) = lo[i];
+    *reinterpret_cast<uint4 *>(o.q_out + at(i) + kD / 2) = hi[i];
+  }
+}
 
 template <int BT>
 __global__ void __launch_bounds__(StoreGeom<BT>::kThreads, 1024 / StoreGeom<BT>::kThreads)
-prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o) {
+prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o, int lead, int page_ctas) {
   using G = StoreGeom<BT>;
   constexpr size_t kHalfPage = static_cast<size_t>(BT) * kQ8TokBytes;
-  __shared__ RowAngles cs[BT];
+  __shared__ RowAngles cs[G::kRows];
+  __shared__ AngleTable table;
+  __shared__ BaseAngle base[G::kQRows][kD / 2];
+  __shared__ int row_pos[G::kQRows], row_run[G::kQRows];
   __shared__ int owner_s, ctx_s, n_s, row0_s;   // the sequence, its context, rows and first row
   __shared__ uint32_t top_s[2][kHkv];
   __shared__ int e_s[2][kHkv], held_s[2][kHkv];   // held: exponent of the page's scale so far
   __shared__ int blk_s;
   pdl_launch_dependents();   // the next kernel may start its own set-up
   const int tid = threadIdx.x;
+  if (tid < kAngles) table.e[tid] = o.table.e[tid];
+  else if (tid < kAngles + kD / 2) table.f[tid - kAngles] = o.table.f[tid - kAngles];
+  const int page_cta = static_cast<int>(blockIdx.x) - lead;
+  if (page_cta < 0 || page_cta >= page_ctas) {
+    rotate_q_rows<BT>(p, o, (page_cta < 0 ? blockIdx.x : blockIdx.x - page_ctas) * G::kQRows, cs, row_pos, row_run, base,
+                      table);
+    pdl_wait_primary();   // this grid ends after the allocation kernel
+    return;
+  }
   if (tid == 0) owner_s = -1;
   if (tid < 2 * kHkv) top_s[tid >> 3][tid & 7] = 0u;
   __syncthreads();
@@ -211,7 +369,7 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o) {
     int ctx, n;
     // (a refused chunk is reported by the allocation kernel)
     if (!chunk_fits<BT>(p, s, &ctx, &n) || n == 0) continue;
-    const long long j = static_cast<long long>(blockIdx.x) - (p.cu_tokens[s] / BT + 2ll * s);
+    const long long j = static_cast<long long>(page_cta) - (p.cu_tokens[s] / BT + 2ll * s);
     if (j < 0 || j > (ctx + n - 1) / BT - ctx / BT) continue;
     mine = s;
     my_ctx = ctx;
@@ -232,57 +390,12 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o) {
   }
   __syncthreads();
   const int ctx = ctx_s;
-  const int page_at = ctx / BT + static_cast<int>(blockIdx.x) - (row0_s / BT + 2 * seq);
+  const int page_at = ctx / BT + page_cta - (row0_s / BT + 2 * seq);
   const int pos0 = max(ctx, page_at * BT);
   const int len = min(ctx + n_s, page_at * BT + BT) - pos0;
   const size_t first = static_cast<size_t>(row0_s) + (pos0 - ctx);   // packed row of pos0
   const int c = tid & 3;
-  auto angles = [&]() {   // one pair a thread
-    const int t = tid / (kD / 2), d = tid % (kD / 2);
-    if (t < len) cs[t].set(d, rope_cos_sin(pos0 + t, p.freqs.f[d]));
-  };
-
-  if (tid >= G::kRole) {
-    // ------------------------------------------------------------------- q
-    const int qt = tid - G::kRole;
-    uint4 lo[G::kQBatch], hi[G::kQBatch];
-    auto q_at = [&](int i) -> size_t {   // item i of the thread: row, head, part c
-      const int item = qt + i * G::kRole;
-      return ((first + (item >> 7)) * kHq + ((item >> 2) & 31)) * kD + 8 * c;
-    };
-    auto held = [&](int i) { return p.q && ((qt + i * G::kRole) >> 7) < len; };
-    auto load = [&](int base) {
-#pragma unroll
-      for (int i = 0; i < G::kQBatch; ++i) {
-        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-        if (held(base + i)) {
-          const uint16_t *row = p.q + q_at(base + i);
-          lo[i] = *reinterpret_cast<const uint4 *>(row);
-          hi[i] = *reinterpret_cast<const uint4 *>(row + kD / 2);
-        }
-      }
-    };
-    load(0);
-    angles();
-    __syncthreads();
-#pragma unroll
-    for (int b = 0; b < G::kQBatches; ++b) {
-      if (b > 0) load(b * G::kQBatch);
-#pragma unroll
-      for (int i = 0; i < G::kQBatch; ++i) {
-        const int it = b * G::kQBatch + i;
-        if (!held(it)) continue;
-        rotate8(&lo[i], &hi[i], cs[(qt + it * G::kRole) >> 7], c);
-        uint16_t *row = o.q_out + q_at(it);
-        *reinterpret_cast<uint4 *>(row) = lo[i];
-        *reinterpret_cast<uint4 *>(row + kD / 2) = hi[i];
-      }
-    }
-    pdl_wait_primary();
-    return;
-  }
-
-  // -------------------------------------------------------------- k and v
+  if (tid < kD / 2) base[0][tid] = base_angle(pos0, p.freqs.f[tid]);
   const int krow = tid >> 5, khead = (tid >> 2) & 7;
   uint4 klo[G::kPasses], khi[G::kPasses], v0[G::kPasses], v1[G::kPasses];
 #pragma unroll
@@ -297,13 +410,25 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o) {
       v1[i] = *reinterpret_cast<const uint4 *>(p.v_new + row + 16 * c + 8);
     }
   }
-  angles();
   // ---- the largest magnitudes of each head's keys (before the rotation) and values
   uint32_t top_k = 0, top_v = 0;
 #pragma unroll
   for (int i = 0; i < G::kPasses; ++i) {
-    top_k = q8_top4(khi[i], q8_top4(klo[i], top_k));
-    top_v = q8_top4(v1[i], q8_top4(v0[i], top_v));
+    top_k = any_top4(khi[i], any_top4(klo[i], top_k));
+    top_v = any_top4(v1[i], any_top4(v0[i], top_v));
+  }
+  top_k = max(top_k & 0xffffu, top_k >> 16);
+  top_v = max(top_v & 0xffffu, top_v >> 16);
+  // rare: infinities and NaN do not count (nor stay plain the keys that a
+  // rotation might make infinite, from 2^126)
+  const bool plain_k = top_k < 0x7e80u, plain_v = top_v < 0x7f80u;
+  if (!plain_k || !plain_v) {
+    top_k = top_v = 0;
+#pragma unroll
+    for (int i = 0; i < G::kPasses; ++i) {
+      top_k = q8_top4(khi[i], q8_top4(klo[i], top_k));
+      top_v = q8_top4(v1[i], q8_top4(v0[i], top_v));
+    }
   }
   top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, 1));
   top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, 2));
@@ -340,16 +465,20 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o) {
     held_s[kv][h] = held;
     if (tid == 0) blk_s = ok ? blk : -1;
   }
+  for (int x = tid; x < len * (kD / 2); x += G::kThreads) {   // (meanwhile)
+    const int t = x / (kD / 2), d = x % (kD / 2);
+    cs[t].set(d, angle_cos_sin(base[0][d], t, table.f[d], table.e));
+  }
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < G::kPasses; ++i) {   // (meanwhile)
+  for (int i = 0; i < G::kPasses; ++i) {
     const int t = krow + i * G::kPassRows;
     if (t < len) rotate8(&klo[i], &khi[i], cs[t], c);
   }
-  asm volatile("bar.sync 1, %0;" ::"n"(G::kRole) : "memory");
   if (blk_s >= 0) {
     unsigned char *page = p.kv + static_cast<size_t>(blk_s) * 2 * kHalfPage;
     // ---- tokens that the page holds already are brought to its new scale
-    for (int x = tid; x < slot0 * 64; x += G::kRole) {   // 16-byte parts: 32 of K, 32 of V a token
+    for (int x = tid; x < slot0 * 64; x += G::kThreads) {   // 16-byte parts: 32 of K, 32 of V a token
       const int t = x >> 6, kv = (x >> 5) & 1, part = x & 31, h = part >> 2;
       const int held = held_s[kv][h], e = e_s[kv][h];
       if (held < kMinExp || held == e) continue;
@@ -369,19 +498,13 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o) {
       if (t >= len) continue;
       unsigned char *row = page + (slot0 + t) * kQ8TokBytes + khead * kQ8HeadBytes;
       if (held_s[0][khead] >= kMinExp) {
-        *reinterpret_cast<uint2 *>(row + 8 * c) =
-            make_uint2(bf16x4_to_e4m3x4(klo[i].x, klo[i].y, inv_k),
-                       bf16x4_to_e4m3x4(klo[i].z, klo[i].w, inv_k));
-        *reinterpret_cast<uint2 *>(row + kD / 2 + 8 * c) =
-            make_uint2(bf16x4_to_e4m3x4(khi[i].x, khi[i].y, inv_k),
-                       bf16x4_to_e4m3x4(khi[i].z, khi[i].w, inv_k));
+        *reinterpret_cast<uint2 *>(row + 8 * c) = quantise8(klo[i], inv_k, plain_k);
+        *reinterpret_cast<uint2 *>(row + kD / 2 + 8 * c) = quantise8(khi[i], inv_k, plain_k);
       }
-      if (held_s[1][khead] >= kMinExp)
-        *reinterpret_cast<uint4 *>(row + kHalfPage + 16 * c) =
-            make_uint4(bf16x4_to_e4m3x4(v0[i].x, v0[i].y, inv_v),
-                       bf16x4_to_e4m3x4(v0[i].z, v0[i].w, inv_v),
-                       bf16x4_to_e4m3x4(v1[i].x, v1[i].y, inv_v),
-                       bf16x4_to_e4m3x4(v1[i].z, v1[i].w, inv_v));
+      if (held_s[1][khead] >= kMinExp) {
+        const uint2 a = quantise8(v0[i], inv_v, plain_v), b = quantise8(v1[i], inv_v, plain_v);
+        *reinterpret_cast<uint4 *>(row + kHalfPage + 16 * c) = make_uint4(a.x, a.y, b.x, b.y);
+      }
     }
   }
   pdl_wait_primary();   // this grid ends after the allocation kernel
@@ -432,7 +555,8 @@ int kv_append_q8_impl(const uint16_t *k_new, const uint16_t *v_new, const uint16
   prm.max_blocks = max_blocks_per_seq;
   prm.num_seqs = num_seqs;
   prm.layer = layer;
-  const Q8Out o{q_out, kv_scales};
+  static const AngleTable table = angle_table(freqs);
+  const Q8Out o{q_out, kv_scales, table};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (launch_pdl(append_alloc_kernel<BT>, dim3(1), dim3(kScanCta), 0, st, prm) != cudaSuccess)
     return PA_ERR_CUDA;
@@ -454,7 +578,7 @@ int prefill_append_q8_impl(const uint16_t *k_new, const uint16_t *v_new, const u
     return PA_ERR_ARG;
   if (static_cast<long long>(max_blocks_per_seq) * BT > INT_MAX) return PA_ERR_ARG;
   if (layer < 0 || layer >= n_layers) return PA_ERR_LAYER;
-  if (num_seqs > (1 << 29)) return PA_ERR_ARG;   // the grid, total_tokens / BT + 2 num_seqs
+  if (num_seqs > (1 << 29)) return PA_ERR_ARG;   // the grid: total_tokens / BT + 2 num_seqs + total_tokens / 8
   if (num_seqs == 0 || total_tokens == 0) return PA_OK;
   if (!k_new || !v_new || !cu_tokens || !kv_cache || !kv_scales || !block_table ||
       !context_lens || !free_list || !free_count || !err || (q_or_null && !q_out))
@@ -484,12 +608,16 @@ int prefill_append_q8_impl(const uint16_t *k_new, const uint16_t *v_new, const u
   prm.max_blocks = max_blocks_per_seq;
   prm.num_seqs = num_seqs;
   prm.layer = layer;
-  const Q8Out o{q_out, kv_scales};
+  static const AngleTable table = angle_table(freqs);
+  const Q8Out o{q_out, kv_scales, table};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (launch_pdl(prefill_alloc_kernel<BT>, dim3(1), dim3(kScanCta), 0, st, prm) != cudaSuccess)
     return PA_ERR_CUDA;
-  if (launch_pdl(prefill_store_q8_kernel<BT>, dim3(total_tokens / BT + 2 * num_seqs),
-                 dim3(StoreGeom<BT>::kThreads), 0, st, prm, o) != cudaSuccess)
+  using G = StoreGeom<BT>;
+  const int page_ctas = total_tokens / BT + 2 * num_seqs;
+  const int q_ctas = q_or_null ? (total_tokens + G::kQRows - 1) / G::kQRows : 0;
+  if (launch_pdl(prefill_store_q8_kernel<BT>, dim3(page_ctas + q_ctas), dim3(G::kThreads), 0, st, prm,
+                 o, std::min(q_ctas, di.sm_count), page_ctas) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
 }
