@@ -36,8 +36,8 @@
 // on with q (each softmax and MMA warp for itself: 229 / 765 us), and the
 // converter's loop skips the multiplication where a page's factor is 1 and the
 // masks in chunks that need none, and stays rolled (unrolled it runs in bursts
-// against the softmax warps: 240 / 790 us).  8 x 2048 tokens 223 us, 617 TFLOP/s
-// (the bf16 kernel over the same values 186), 32 x 512 after 4096 747 us, 782
+// against the softmax warps: 240 / 790 us).  8 x 2048 tokens 218 us, 631 TFLOP/s
+// (the bf16 kernel over the same values 186), 32 x 512 after 4096 742 us, 787
 // TFLOP/s (629).  Tried and slower: K's bytes as the tensor core's own e4m3 operand
 // against q in two e4m3 parts, which halves the converter's work but leaves the
 // pages' K scales to the softmax, whose registers they outgrow (267 / 815 us).
@@ -782,9 +782,20 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           mbar_arrive(&sm.s_free[h]);           // S_{j+1} may land in the S columns
           if (!full) {
             // masked keys: -inf (loaded K rows past the tile or in a missing page may be anything)
+            if (pm != static_cast<int>(kAllPages)) {
 #pragma unroll
-            for (int c = 0; c < kChunk; ++c)
-              if (!((c <= lim) && ((pm >> (c / BT)) & 1))) v[c] = 0xff800000u;
+              for (int c = 0; c < kChunk; ++c)
+                if (!((pm >> (c / BT)) & 1)) v[c] = 0xff800000u;
+            }
+            // (the warp's rows are 8 tokens: columns before the first one's need no test)
+            const int lim0 = __shfl_sync(0xffffffffu, lim, 0);
+#pragma unroll
+            for (int c0 = 0; c0 < kChunk; c0 += 16)
+              if (c0 + 15 > lim0) {
+#pragma unroll
+                for (int c = c0; c < c0 + 16; ++c)
+                  if (c > lim) v[c] = 0xff800000u;
+              }
           }
           // row maximum: 8 chains of three-input maxima over keys q, q+8, ..
           float mx8[8];
