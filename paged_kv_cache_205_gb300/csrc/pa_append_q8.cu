@@ -28,13 +28,15 @@ constexpr int kAngles = 64;
 struct AngleTable {
   float2 e[kAngles];
   float2 f[kD / 2];
+  double2 exact[kAngles];   // (cos, sin) again
 };
 
 AngleTable angle_table(const RopeFreqs &freqs) {
   AngleTable t;
   for (int i = 0; i < kAngles; ++i) {
     const double a = i * (6.283185307179586476925 / kAngles);
-    t.e[i] = make_float2(static_cast<float>(std::cos(a)), static_cast<float>(std::sin(a)));
+    t.exact[i] = make_double2(std::cos(a), std::sin(a));
+    t.e[i] = make_float2(static_cast<float>(t.exact[i].x), static_cast<float>(t.exact[i].y));
   }
   for (int d = 0; d < kD / 2; ++d) {
     t.f[d].x = static_cast<float>(freqs.f[d]);
@@ -96,6 +98,79 @@ __device__ __forceinline__ float2 angle_cos_sin(const BaseAngle &b, int step, fl
   const float cm1 = r2 * fmaf(r2, 1.f / 24, -0.5f);                      // cos r - 1
   const float sn = fmaf(r * r2, fmaf(r2, 1.f / 120, -1.f / 6), r);       // sin r
   return make_float2(e.x + fmaf(e.x, cm1, -e.y * sn), e.y + fmaf(e.y, cm1, e.x * sn));
+}
+
+// A key's byte rounds twice, to bf16 and to e4m3, and an error of the fp32 rotation
+// changes it only where the value lies next to a bf16 border beside an e4m3
+// border: mantissa bits 0x78000 and 0x88000 (of 20; bytes below e4m3's normal range
+// have theirs elsewhere, and steps that weigh nothing).  near_border is below 2 kNear
+// within kNear ulps of one.  The fp32 error is mostly below 2^-24 (|a| + |b|), which
+// is 4 ulps where the products cancel to a quarter; the few words of a prompt's keys
+// that near a border (one in 16,000) are rotated again in fp64, 2% of the call's
+// time, and 8 x 2048 tokens' bytes then differ from the definition's in 2 of 17
+// million, both where the products cancel to 2^-6 and less (7 without).
+constexpr uint32_t kNear = 4;
+__device__ __forceinline__ uint32_t near_border(float x) {
+  return (__float_as_uint(x) + (0x88000u + kNear)) & 0xeffffu;   // (both borders at 0)
+}
+
+// x to fp32 so that a later rounding to fewer bits comes out as x's own.
+__device__ __forceinline__ float round_to_odd(double x) {
+  const float f = __double2float_rz(x);
+  return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// The bytes of a pair of key elements (a, b) rotated by the angle pos * f in fp64,
+// the first in the low byte.
+__device__ __forceinline__ uint32_t exact_key_pair(float a, float b, int pos, double f, float inv,
+                                                const double2 *table) {
+  constexpr double kStepHi = 6.283185307179586232 / kAngles;
+  constexpr double kStepLo = 2.4492935982947064e-16 / kAngles;
+  const double angle = static_cast<double>(pos) * f;
+  const double k = rint(angle * (0.15915494309189533577 * kAngles));
+  const double r = fma(-k, kStepLo, fma(-k, kStepHi, angle)), r2 = r * r;
+  const double2 e = table[static_cast<int>(static_cast<long long>(k) & (kAngles - 1))];
+  // Taylor sums for |r| <= pi / 64: r^9 / 9! < 2^-57, r^10 / 10! < 2^-65
+  const double cm1 = r2 * fma(r2, fma(r2, fma(r2, 1. / 40320, -1. / 720), 1. / 24), -0.5);
+  const double sn = fma(r * r2, fma(r2, fma(r2, -1. / 5040, 1. / 120), -1. / 6), r);
+  const double c = e.x + fma(e.x, cm1, -e.y * sn), s = e.y + fma(e.y, cm1, e.x * sn);
+  const double da = a, db = b;
+  const float2 t = bf16x2_to_float2(
+      float2_to_bf16x2(round_to_odd(fma(da, c, -db * s)), round_to_odd(fma(db, c, da * s))));
+  return e4m3x2(t.x * inv, t.y * inv);
+}
+
+// Pairs d and d + 1 (d even) of the key at k, rotated so, into its bytes at row.
+__device__ __forceinline__ void exact_key_word(const uint16_t *k, unsigned char *row, int d, int pos,
+                                               float inv, const RopeFreqs &freqs,
+                                               const double2 *table) {
+#pragma unroll 1
+  for (int i = d; i < d + 2; ++i) {
+    const uint32_t x =
+        exact_key_pair(__uint_as_float(static_cast<uint32_t>(k[i]) << 16),
+                       __uint_as_float(static_cast<uint32_t>(k[i + kD / 2]) << 16), pos, freqs.f[i], inv, table);
+    row[i] = static_cast<unsigned char>(x);
+    row[i + kD / 2] = static_cast<unsigned char>(x >> 8);
+  }
+}
+
+// The pairs (lo, hi) of one bf16 word each, rotated by (x, y) and (z, w).
+__device__ __forceinline__ void rotate2(uint32_t *lo, uint32_t *hi, float4 cs) {
+  const float2 a = bf16x2_to_float2(*lo), b = bf16x2_to_float2(*hi);
+  *lo = float2_to_bf16x2(fmaf(a.x, cs.x, -b.x * cs.y), fmaf(a.y, cs.z, -b.y * cs.w));
+  *hi = float2_to_bf16x2(fmaf(b.x, cs.x, a.x * cs.y), fmaf(b.y, cs.z, a.y * cs.w));
+}
+
+// The same for keys; bit `bit` of *borders: one of the four nears a border.
+__device__ __forceinline__ void rotate2_key(uint32_t *lo, uint32_t *hi, float4 cs, int bit,
+                                            uint32_t *borders) {
+  const float2 a = bf16x2_to_float2(*lo), b = bf16x2_to_float2(*hi);
+  const float l0 = fmaf(a.x, cs.x, -b.x * cs.y), l1 = fmaf(a.y, cs.z, -b.y * cs.w);
+  const float h0 = fmaf(b.x, cs.x, a.x * cs.y), h1 = fmaf(b.y, cs.z, a.y * cs.w);
+  if (min(min(near_border(l0), near_border(l1)), min(near_border(h0), near_border(h1))) < 2 * kNear)
+    *borders |= 1u << bit;
+  *lo = float2_to_bf16x2(l0, l1);
+  *hi = float2_to_bf16x2(h0, h1);
 }
 
 // (lo, hi) of 4 consecutive pairs of one head row: bf16 words of dims
@@ -221,19 +296,21 @@ struct __align__(16) RowAngles {
   }
 };
 
-// The pairs (lo, hi) of one bf16 word each, rotated by (x, y) and (z, w).
-__device__ __forceinline__ void rotate2(uint32_t *lo, uint32_t *hi, float4 cs) {
-  const float2 a = bf16x2_to_float2(*lo), b = bf16x2_to_float2(*hi);
-  *lo = float2_to_bf16x2(fmaf(a.x, cs.x, -b.x * cs.y), fmaf(a.y, cs.z, -b.y * cs.w));
-  *hi = float2_to_bf16x2(fmaf(b.x, cs.x, a.x * cs.y), fmaf(b.y, cs.z, a.y * cs.w));
-}
-
 // 16 bytes (8 bf16) of one half of a head row, rotated against the other half.
 __device__ __forceinline__ void rotate8(uint4 *lo, uint4 *hi, const RowAngles &r, int c) {
   rotate2(&lo->x, &hi->x, r.a[c]);
   rotate2(&lo->y, &hi->y, r.a[4 + c]);
   rotate2(&lo->z, &hi->z, r.a[8 + c]);
   rotate2(&lo->w, &hi->w, r.a[12 + c]);
+}
+
+// The same for keys: bits bit .. bit + 3.
+__device__ __forceinline__ void rotate8_key(uint4 *lo, uint4 *hi, const RowAngles &r, int c, int bit,
+                                            uint32_t *borders) {
+  rotate2_key(&lo->x, &hi->x, r.a[c], bit, borders);
+  rotate2_key(&lo->y, &hi->y, r.a[4 + c], bit + 1, borders);
+  rotate2_key(&lo->z, &hi->z, r.a[8 + c], bit + 2, borders);
+  rotate2_key(&lo->w, &hi->w, r.a[12 + c], bit + 3, borders);
 }
 
 __device__ __forceinline__ uint32_t q8_top4(uint4 w, uint32_t top) {
@@ -268,9 +345,9 @@ __device__ __forceinline__ uint2 quantise8(uint4 w, float inv, bool plain) {
 // page CTAs, which meanwhile wait for the pages that the allocation kernel hands
 // out, and the rest after them.  CTAs of 64 registers, four (256 threads) an SM.
 // Bound by memory and by each CTA's chain of load, angle, maximum, table entry and
-// store: 8 x 2048 tokens 32.9 us, 184 MB at 5.6 TB/s (no q CTA first 34.7, 304
+// store: 8 x 2048 tokens 33.6 us, 184 MB at 5.5 TB/s (no q CTA first 34.7, 304
 // first 33.2; q in the page CTAs, every row's angles in fp64 36.5; a CTA per window
-// of rows with every warp on k, v and q in turn 53), 31 tokens 6.4 us.
+// of rows with every warp on k, v and q in turn 53), 31 tokens 6.5 to 7.4 us.
 template <int BT>
 struct StoreGeom {
   static constexpr int kThreads = BT == 32 ? 512 : 256;
@@ -286,7 +363,8 @@ struct StoreGeom {
 template <int BT>
 __device__ __forceinline__ void rotate_q_rows(const PrefillAppendParams &p, const Q8Out &o, int r0,
                                               RowAngles *cs, int *row_pos, int *row_run,
-                                              BaseAngle (*base)[kD / 2], const AngleTable &table) {
+                                              BaseAngle (*base)[kD / 2], const float2 *table_f,
+                                              const float2 *table_e) {
   using G = StoreGeom<BT>;
   const int tid = threadIdx.x, c = tid & 3;
   uint4 lo[G::kQParts], hi[G::kQParts];
@@ -325,7 +403,7 @@ __device__ __forceinline__ void rotate_q_rows(const PrefillAppendParams &p, cons
   for (int x = tid; x < G::kQRows * (kD / 2); x += G::kThreads) {
     const int t = x / (kD / 2), d = x % (kD / 2);
     if (row_pos[t] < 0) continue;
-    cs[t].set(d, angle_cos_sin(base[row_run[t]][d], t - row_run[t], table.f[d], table.e));
+    cs[t].set(d, angle_cos_sin(base[row_run[t]][d], t - row_run[t], table_f[d], table_e));
   }
   __syncthreads();
 #pragma unroll
@@ -343,7 +421,7 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o, int lead, int page_ctas)
   using G = StoreGeom<BT>;
   constexpr size_t kHalfPage = static_cast<size_t>(BT) * kQ8TokBytes;
   __shared__ RowAngles cs[G::kRows];
-  __shared__ AngleTable table;
+  __shared__ float2 table_e[kAngles], table_f[kD / 2];
   __shared__ BaseAngle base[G::kQRows][kD / 2];
   __shared__ int row_pos[G::kQRows], row_run[G::kQRows];
   __shared__ int owner_s, ctx_s, n_s, row0_s;   // the sequence, its context, rows and first row
@@ -352,12 +430,12 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o, int lead, int page_ctas)
   __shared__ int blk_s;
   pdl_launch_dependents();   // the next kernel may start its own set-up
   const int tid = threadIdx.x;
-  if (tid < kAngles) table.e[tid] = o.table.e[tid];
-  else if (tid < kAngles + kD / 2) table.f[tid - kAngles] = o.table.f[tid - kAngles];
+  if (tid < kAngles) table_e[tid] = o.table.e[tid];
+  else if (tid < kAngles + kD / 2) table_f[tid - kAngles] = o.table.f[tid - kAngles];
   const int page_cta = static_cast<int>(blockIdx.x) - lead;
   if (page_cta < 0 || page_cta >= page_ctas) {
     rotate_q_rows<BT>(p, o, (page_cta < 0 ? blockIdx.x : blockIdx.x - page_ctas) * G::kQRows, cs, row_pos, row_run, base,
-                      table);
+                      table_f, table_e);
     pdl_wait_primary();   // this grid ends after the allocation kernel
     return;
   }
@@ -467,13 +545,14 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o, int lead, int page_ctas)
   }
   for (int x = tid; x < len * (kD / 2); x += G::kThreads) {   // (meanwhile)
     const int t = x / (kD / 2), d = x % (kD / 2);
-    cs[t].set(d, angle_cos_sin(base[0][d], t, table.f[d], table.e));
+    cs[t].set(d, angle_cos_sin(base[0][d], t, table_f[d], table_e));
   }
   __syncthreads();
+  uint32_t borders = 0;   // bit 4 i + w: word w of row i's parts
 #pragma unroll
   for (int i = 0; i < G::kPasses; ++i) {
     const int t = krow + i * G::kPassRows;
-    if (t < len) rotate8(&klo[i], &khi[i], cs[t], c);
+    if (t < len) rotate8_key(&klo[i], &khi[i], cs[t], c, 4 * i, &borders);
   }
   if (blk_s >= 0) {
     unsigned char *page = p.kv + static_cast<size_t>(blk_s) * 2 * kHalfPage;
@@ -505,6 +584,15 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o, int lead, int page_ctas)
         const uint2 a = quantise8(v0[i], inv_v, plain_v), b = quantise8(v1[i], inv_v, plain_v);
         *reinterpret_cast<uint4 *>(row + kHalfPage + 16 * c) = make_uint4(a.x, a.y, b.x, b.y);
       }
+    }
+    if (!plain_k || held_s[0][khead] < kMinExp) borders = 0;
+#pragma unroll 1
+    for (; borders; borders &= borders - 1) {
+      const int i = (__ffs(borders) - 1) >> 2, d = 8 * c + 2 * ((__ffs(borders) - 1) & 3);
+      const int t = krow + i * G::kPassRows;
+      exact_key_word(p.k_new + ((first + t) * kHkv + khead) * kD,
+                     page + (slot0 + t) * kQ8TokBytes + khead * kQ8HeadBytes, d, pos0 + t, inv_k, p.freqs,
+                     o.table.exact);
     }
   }
   pdl_wait_primary();   // this grid ends after the allocation kernel
