@@ -565,7 +565,9 @@ int pa_decode_set_test_plan(int mode);
  * at any position).  A value is stored as the e4m3 number nearest to value /
  * scale (ties to even; at most half a step, 2^-4 of the value, off down to
  * 2^-15 of the page's largest); NaN and infinities are stored as NaN and do
- * not count for the scale.
+ * not count for the scale.  The attention calls take scales as the appends
+ * write them (powers of two from 2^-117 to 2^120; outputs are undefined for
+ * others).
  */
 
 /*
@@ -600,7 +602,8 @@ int pa_prefill_append_rope_q8(const uint16_t *k_new, const uint16_t *v_new,
 /*
  * pa_decode_attention_q8 -- pa_decode_attention over the 8-bit cache: q and
  * out stay bf16, sums and the softmax are fp32.  A sequence with context 0
- * gets a zero output, and so does one none of whose pages is valid.
+ * gets a zero output, and so does one none of whose pages is valid.  A q head
+ * that is not finite has a NaN output.
  * num_seqs is at most 2048.  workspace: pa_decode_workspace_size_q8 bytes of
  * scratch whose contents do not matter; calls that overlap in time must not
  * share it.
@@ -617,7 +620,9 @@ size_t pa_decode_workspace_size_q8(int num_seqs, int max_blocks_per_seq, int blo
  * pa_prefill_attention_q8 -- pa_prefill_attention over the 8-bit cache (the
  * chunk's own K/V already in it: pa_prefill_append_rope_q8 before this call
  * on the same stream).  Same limits, errors and handling of refused chunks;
- * pa_prefill_set_test_fault acts on it too.
+ * a q row that is not finite has a NaN output, and a NaN key or value makes
+ * the rows that see it NaN and no others; pa_prefill_set_test_fault acts on
+ * it too.
  */
 int pa_prefill_attention_q8(uint16_t *out, const uint16_t *q, int total_tokens,
                             const int32_t *cu_tokens, const uint8_t *kv_cache,

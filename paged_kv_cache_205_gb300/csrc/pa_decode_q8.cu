@@ -22,6 +22,8 @@
 //                piece costs 8.4 KiB of partial written and read again
 //   26.9 / 53.5  the plan made, and 4 tiles a CTA prefetched, while the kernels
 //                before end (2 rows of 14 to 17 tokens, direct: 5.5 to 3.5)
+//   26.3 / 49.9  the reference below the largest score (fewer moves), shared
+//                memory addressed as such
 // Of the 53.5: 4.4 to the first data, 37 at 7.1 TB/s, 5 between the CTAs' last
 // tiles (SMs of unequal speed), 5 to end, launch and run the merge.
 // The copies' rows are two heads wide (128 bytes): the TMA unit takes a box row
@@ -75,7 +77,7 @@ constexpr int kDirectTiles = 8;            // longest table served by one CTA a 
 constexpr int kPrefetchTiles = 4;          // tiles brought into L2 before the wait
 constexpr int kTileBytes = 2 * kTile * kQ8TokBytes;   // K and V of 8 heads: 16 KiB
 constexpr int kPairBytes = 2 * kQ8HeadBytes;          // one token, two heads: a row of the copies
-constexpr float kNoScore = -1e30f;       // the reference before a score is seen
+constexpr float kNoScore = -3e38f;       // the reference before a score is seen
 constexpr float kBelow = 7.f;            // log2 units the reference is set below the largest score
 constexpr float kMove = 15.f;            // and a score may lie above it
 constexpr float kLog2e = 1.4426950408889634f;
@@ -207,7 +209,8 @@ struct State {
 };
 
 // q head g of the group in f16, scaled by a power of two to [2^12, 2^13);
-// returns the head's score factor: qscale / that power.  Lane c holds dims
+// returns the head's score factor: qscale / that power, or NaN for a head that is
+// not finite (its scores are NaN, or all -inf: so is its output).  Lane c holds dims
 // 16c .. 16c+15 (the order of the K loads): B's columns of S^T.  q_group: the
 // group's q in shared memory.
 __device__ __forceinline__ float load_q(uint32_t q_group, int g, int c, float qscale,
@@ -221,7 +224,8 @@ __device__ __forceinline__ float load_q(uint32_t q_group, int g, int c, float qs
   const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = q8_top(w[i], top);
+  for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const int f = min(266 - static_cast<int>(top >> 7), 253);   // exponent field of the factor
@@ -231,7 +235,7 @@ __device__ __forceinline__ float load_q(uint32_t q_group, int g, int c, float qs
     const float2 x = bf16x2_to_float2(w[i]);
     qa[i] = f16x2(x.x * up, x.y * up);
   }
-  return qscale * down;
+  return top < 0x7f80u ? qscale * down : __int_as_float(0x7fc00000);
 }
 
 // Folds a tile into the state.  k0 / k1: the head pair's K rows of tokens 0..7

@@ -57,6 +57,7 @@ constexpr int kQThreads = 16 * 32;
 // A score factor's floor: a masked score (-inf) times it stays -inf, and a score
 // of at most 2^28 times it is as good as 0.
 constexpr float kTiny = 1.2e-38f;
+constexpr float kLargeFactor = 0.015625f;   // 2^-6
 // Register budget: 512 threads x 128 at launch; the softmax warpgroups take
 // kQRegsSoft, the producer/MMA warpgroup and the converters give up to theirs.
 constexpr int kQRegsSoft = 192;
@@ -98,11 +99,11 @@ struct __align__(1024) QSmem {
   uint16_t order[kSortQ];                          // tiles, heaviest first
   uint8_t tile_bins[kSortQ];                       // each tile's bin
   uint2 raw_mul[kRaw][kChunk / 8];                 // per page: f16x2 factors of K's and V's bytes
-  float raw_lv[kRaw][kChunk / 8];                  // per page: log2 of V's scale
+  float raw_lv[kRaw][kChunk / 8];                  // per page: log2 of what its V bytes still lack
   RawChunk raw_rec[kRaw];
   ItemRec item[kQBufs];
   float4 scale[kWide];                             // (sK, log2 sV, 1 / sV, 1: V's pages far apart)
-  float lv[kWide][kChunk / 8];                     // far apart: log2 of V's scale per page
+  float lv[kWide][kChunk / 8];
   uint8_t q_exp[kQBufs][kHalves][kRows];           // per row: exponent field of its largest |q|
   // per dim: the first position in an item's diagonal chunks whose value is NaN,
   // below the item's number inverted (a later item's record is the smaller one)
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           if (lane < kPagesPerChunk) {
             sm.raw_mul[st][lane] = make_uint2(pow2_f16x2(valid ? ek - top_k : 0),
                                               pow2_f16x2(valid && !far ? ev - top_v : 0));
-            sm.raw_lv[st][lane] = static_cast<float>((valid ? ev : top_v) - 127);
+            sm.raw_lv[st][lane] = static_cast<float>((valid && far ? ev : top_v) - 127);
           }
           __syncwarp();
           if (lane == 0) {
@@ -737,7 +738,6 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         const int lim = qpos - kbase;           // keys c <= lim are at or before the row
         const float4 sc = sm.scale[st];         // sK, log2 sV, 1 / sV, V's pages far apart
         const float fk = fmaxf(factor * sc.x, kTiny);
-        const float2 f2 = make_float2(fk, fk);
         bool pv_done = j == 0;                  // PV_{j-1} complete: O stable, P columns read
         auto wait_pv = [&]() -> bool {
           if (pv_done) return true;
@@ -772,7 +772,9 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         };
         // P = 2^(s f sK + log2 sV - m) in f16 pairs (key 2c in the low half of
         // column c) goes into the half's P columns of tensor memory.
-        if (sc.w == 0.f) {
+        // A fused product keeps m's rounding error: below 2^-2 for scores up to 2^22,
+        // which fk bounds (|S| < 2^28), but enough to overflow the exponential above.
+        if (!__any_sync(0xffffffffu, sc.w != 0.f || fk > kLargeFactor)) {
           uint32_t v[kChunk];
 #pragma unroll
           for (int c0 = 0; c0 < kChunk; c0 += 32)
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             break;
           }
           const float bias = sc.y - ((m == p_neg_inf()) ? 0.f : m);
-          const float2 b2 = make_float2(bias, bias);
+          const float2 b2 = make_float2(bias, bias), f2 = make_float2(fk, fk);
           float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                           make_float2(0.f, 0.f)};
           uint32_t pw[kChunk / 2];
@@ -834,8 +836,8 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           l = fmaf(((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) +
                        ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y)), sc.z, l);
         } else {
-          // pages far apart: log2 sV page by page, S read twice, 8 keys at a
-          // time (rare, so kept small)
+          // pages far apart (log2 sV page by page) or huge scores (each rounded
+          // as m is): S read twice, 8 keys at a time (rare, so kept small)
           auto load8 = [&](int c0, float (&x)[8]) {
             uint32_t u[8];
             tc::tmem_ld8(s_addr + c0, u);
@@ -852,7 +854,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             float mx = x[0];
 #pragma unroll
             for (int c = 1; c < 8; ++c) mx = fmaxf(mx, x[c]);
-            mc = fmaxf(mc, fmaf(mx, fk, sm.lv[st][c0 / BT]));
+            mc = fmaxf(mc, __fadd_rn(__fmul_rn(mx, fk), sm.lv[st][c0 / BT]));
           }
           if (!move_to(mc) || !wait_pv()) {
             ok = false;
@@ -867,8 +869,8 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             uint32_t w[4];
 #pragma unroll
             for (int c = 0; c < 8; c += 2) {
-              const float e0 = p_exp2(fmaf(x[c], fk, lv - base));
-              const float e1 = p_exp2(fmaf(x[c + 1], fk, lv - base));
+              const float e0 = p_exp2(__fadd_rn(__fmul_rn(x[c], fk), lv) - base);
+              const float e1 = p_exp2(__fadd_rn(__fmul_rn(x[c + 1], fk), lv) - base);
               sum += e0 + e1;
               w[c >> 1] = pack_f16(e0, e1);
             }

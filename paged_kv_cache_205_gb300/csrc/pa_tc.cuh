@@ -53,13 +53,6 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t start, uint32_t lbo, ui
   return d;
 }
 
-// The same in the 64-byte swizzled layout (16-byte chunk c of a 64-byte row r
-// stored at chunk c ^ (r / 2 & 3); 8 rows = 512 bytes).
-__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t start, uint32_t lbo, uint32_t sbo) {
-  return (sdesc_sw128(start, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) |
-         (static_cast<uint64_t>(4) << 61);
-}
-
 // Instruction descriptor of a dense MMA: A and B bf16, D fp32, A K-major,
 // B K-major or MN-major, M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major) {
@@ -75,9 +68,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major)
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return idesc_bf16(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
-
-// A and B e4m3 (kind::f8f6f4), both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) { return idesc_f16(M, N, false); }
 
 // One lane of a converged warp (every lane must take part): the lane that
 // issues tcgen05 operations.  Issued this way, from a warp known to be
@@ -100,17 +90,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The same with 8-bit floating-point operands, K = 32.
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }

@@ -152,6 +152,23 @@ def test_decode_nan_and_zero_scores():
     assert np.all(np.abs(got[1] - mean) <= bf16_half_ulp(mean) + np.abs(v).max() * 2.0 ** -12)
 
 
+@pytest.mark.parametrize("bad", [0x7F80, 0xFF80, 0x7FC0])
+@pytest.mark.parametrize("lens", [[20, 1, 9], [2000, 40, 700]], ids=["short", "long"])
+def test_decode_q_head_not_finite(bad, lens):
+    """An infinity or NaN in a q head makes that head's output NaN and changes no other."""
+    rng, pool, scales, table, _ = _cache(9, lens, 16)
+    q = wl.normal_bf16(rng, (3, N_Q, D))
+    want, _ = _decode(q, pool, scales, table, lens)
+    q = q.copy()
+    q[0, 9, 3] = q[1, 31, 63] = bad
+    got, err = _decode(q, pool, scales, table, lens)
+    assert err == 0
+    heads = np.zeros((3, N_Q), bool)
+    heads[0, 9] = heads[1, 31] = True
+    assert np.isnan(got[heads]).all()
+    assert np.array_equal(got[~heads], want[~heads])
+
+
 @pytest.mark.parametrize("page", PAGES)
 def test_decode_bad_pages_and_contexts(page):
     """A page id out of range drops its tokens and is reported; a sequence
@@ -635,6 +652,47 @@ def test_prompts_then_decode_steps_then_free(page):
     _, _, bt, count, err = st.host()
     assert err == 0 and count == blocks and np.all(bt == -1)
     assert np.array_equal(np.sort(st.fl.cpu().numpy()), np.arange(blocks))
+
+
+# ------------------------------------------------------------ scores of any size
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("exponent", [30, 60, 110], ids=["2^30", "2^60", "2^110"])
+@pytest.mark.parametrize("negative", [False, True], ids=["", "negative"])
+def test_scores_beyond_the_exponential(page, exponent, negative):
+    """Scores of about 2^exponent, all negative in one case: a row's weight is all
+    on its largest score (the next lies 2^-9 of it below, 2^21 and more: its weight
+    is 0 in fp64 too), however coarse fp32's steps are there.  Rows whose two
+    largest scores are closer (fp32 sums of 64 products are off by up to 2^-17 of
+    the largest) are not looked at."""
+    lens = [50, 137]
+    rng, pool, scales, table, _ = _cache(101 + page, lens, page, poison=False)
+    scales[:, 0] = 2.0 ** (exponent // 2)
+    if negative:
+        pool[:, 0] &= 0x7F
+    q = np.abs(rng.standard_normal((sum(lens), N_Q, D))) if negative else rng.standard_normal((sum(lens), N_Q, D))
+    q = oracle.f64_to_bf16((-1 if negative else 1) * q * 2.0 ** (exponent - exponent // 2 - 8))
+    vals, qf = q8.decode(pool, scales), oracle.bf16_to_f64(q)
+    got, err = _prefill(q, _cu(lens), pool, scales, table, [0, 0])
+    last = [lens[0] - 1, sum(lens) - 1]
+    dec, err2 = _decode(q[last], pool, scales, table, lens)
+    assert err == err2 == 0
+    looked = 0
+    for s, (r0, n) in enumerate(zip([0, lens[0]], lens)):
+        kv = vals[table[s, 0, :-(-n // page)]]
+        keys, values = (kv[:, j].reshape(-1, N_KV, D)[:n] for j in (0, 1))
+        for h in range(N_Q):
+            z = qf[r0:r0 + n, h] @ keys[:, h // 4].T * 0.125
+            z[np.triu_indices(n, 1)] = -np.inf
+            order = np.sort(z, -1)
+            rows = np.arange(n)
+            apart = rows[(rows == 0) | (order[:, -1] - order[:, -2] > 2.0 ** -9 * np.abs(z[z > -np.inf]).max())]
+            want = values[z[apart].argmax(-1), h // 4]
+            tol = bf16_half_ulp(want)
+            assert np.all(np.abs(got[r0 + apart, h] - want) <= tol)
+            if n - 1 in apart:
+                assert np.all(np.abs(dec[s, h] - want[-1]) <= tol[-1])
+            looked += len(apart)
+    assert looked > N_Q * sum(lens) // 4
 
 
 # ------------------------------------------------------------ ways to call them
