@@ -58,6 +58,9 @@ constexpr int kQThreads = 16 * 32;
 // of at most 2^28 times it is as good as 0.
 constexpr float kTiny = 1.2e-38f;
 constexpr float kLargeFactor = 0.015625f;   // 2^-6
+// V scales below 2^-94 (exponent field 33) leave the rest to V's f16 values, so
+// that l = sum P / sV stays in fp32's range (2^15 2^94 for each of 2^18 keys).
+constexpr int kLeastV = 33;
 // Register budget: 512 threads x 128 at launch; the softmax warpgroups take
 // kQRegsSoft, the producer/MMA warpgroup and the converters give up to theirs.
 constexpr int kQRegsSoft = 192;
@@ -429,12 +432,13 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           // the chunk's scales are its largest page's (exponent fields)
           const int ek = __float_as_int(now.sk) >> 23, ev = __float_as_int(now.sv) >> 23;
           const int top_k = __reduce_max_sync(0xffffffffu, valid ? ek : 1);
-          const int top_v = __reduce_max_sync(0xffffffffu, valid ? ev : 1);
-          const bool far = __reduce_min_sync(0xffffffffu, valid ? ev : top_v) < top_v - 7;
+          const int ev1 = max(ev, kLeastV);
+          const int top_v = __reduce_max_sync(0xffffffffu, valid ? ev1 : kLeastV);
+          const bool far = __reduce_min_sync(0xffffffffu, valid ? ev1 : top_v) < top_v - 7;
           if (lane < kPagesPerChunk) {
             sm.raw_mul[st][lane] = make_uint2(pow2_f16x2(valid ? ek - top_k : 0),
-                                              pow2_f16x2(valid && !far ? ev - top_v : 0));
-            sm.raw_lv[st][lane] = static_cast<float>((valid && far ? ev : top_v) - 127);
+                                              pow2_f16x2(!valid ? 0 : ev - (far ? ev1 : top_v)));
+            sm.raw_lv[st][lane] = static_cast<float>((valid && far ? ev1 : top_v) - 127);
           }
           __syncwarp();
           if (lane == 0) {

@@ -654,6 +654,30 @@ def test_prompts_then_decode_steps_then_free(page):
     assert np.array_equal(np.sort(st.fl.cpu().numpy()), np.arange(blocks))
 
 
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("far", [False, True], ids=["", "far"])
+def test_smallest_value_scales(page, far):
+    """Values of 2^-110 (the smallest scale), alone and beside pages of 2^-90.
+    The prefill kernel holds what lies below 2^-94 of a scale in f16 values whose
+    last step is 2^-24: half of it, 2^-25 2^-94, comes to the bound."""
+    lens = [300, 20]
+    rng, pool, scales, table, _ = _cache(55 + page, lens, page)
+    scales[:, 1] = 2.0 ** -117
+    if far:
+        scales[::3, 1] = 2.0 ** -97
+    q = wl.normal_bf16(rng, (sum(lens), N_Q, D))
+    ref, _ = oracle.prefill_attention(q, _cu(lens), q8.pool_bf16(pool, scales), table, [0, 0], 0, block_tokens=page)
+    got, err = _prefill(q, _cu(lens), pool, scales, table, [0, 0])
+    assert err == 0 and np.abs(ref).max() < 2.0 ** -85 and np.all(np.abs(ref).max(-1) > 0)
+    v = np.abs(q8.decode(pool, scales))
+    s = 0.125 * np.abs(oracle.bf16_to_f64(q)).sum(-1).max() * np.nanmax(v[:, 0])
+    tol = bf16_half_ulp(ref) + np.nanmax(v[:, 1]) * (2.0 ** -12 + 300 * 2.0 ** -25 + s * 2.0 ** -16) + 2.0 ** -119
+    assert np.all(np.abs(got - ref) <= tol)
+    last = [lens[0] - 1, sum(lens) - 1]
+    dec, err = _decode(q[last], pool, scales, table, lens)
+    assert err == 0 and np.all(np.abs(dec - ref[last]) <= tol[last])
+
+
 # ------------------------------------------------------------ scores of any size
 @pytest.mark.parametrize("page", PAGES)
 @pytest.mark.parametrize("exponent", [30, 60, 110], ids=["2^30", "2^60", "2^110"])
