@@ -359,6 +359,23 @@ struct StoreGeom {
   static_assert(kPassRows * kPasses == BT && kThreads * kQParts == kQRows * kHq * 4, "");
 };
 
+// The number of s in [lo, hi) with start(s) <= x, plus lo, for start that does not
+// decrease: every thread of the CTA probes, so that each round divides the range
+// by their number.
+template <int kThreads, class Start>
+__device__ __forceinline__ int first_after(int lo, int hi, int x, Start start) {
+  while (hi - lo > kThreads) {
+    const int step = (hi - lo + kThreads - 1) / kThreads;
+    const long long s = lo + static_cast<long long>(threadIdx.x) * step;
+    const int c = __syncthreads_count(s < hi && start(static_cast<int>(s)) <= x);
+    if (c == 0) return lo;
+    lo += (c - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  const int s = lo + threadIdx.x;
+  return lo + __syncthreads_count(s < hi && start(s) <= x);
+}
+
 // The packed rows [r0, r0 + kQRows) of q, rotated.
 template <int BT>
 __device__ __forceinline__ void rotate_q_rows(const PrefillAppendParams &p, const Q8Out &o, int r0,
@@ -382,8 +399,14 @@ __device__ __forceinline__ void rotate_q_rows(const PrefillAppendParams &p, cons
     }
   }
   if (tid < G::kQRows) row_pos[tid] = -1;   // rows of refused chunks stay as they are
+  int s0 = 0, s1 = p.num_seqs;
+  if (s1 > G::kThreads) {   // the sequences that may have rows here
+    auto start = [&](int s) { return p.cu_tokens[s]; };
+    s0 = max(first_after<G::kThreads>(0, s1, r0, start) - 1, 0);
+    s1 = first_after<G::kThreads>(s0, s1, r0 + G::kQRows - 1, start);
+  }
   __syncthreads();
-  for (int s = tid; s < p.num_seqs; s += G::kThreads) {
+  for (int s = s0 + tid; s < s1; s += G::kThreads) {
     const int a = p.cu_tokens[s], b = p.cu_tokens[s + 1];
     if (a >= r0 + G::kQRows || b <= r0) continue;
     int ctx, n;
@@ -442,8 +465,13 @@ prefill_store_q8_kernel(PrefillAppendParams p, Q8Out o, int lead, int page_ctas)
   if (tid == 0) owner_s = -1;
   if (tid < 2 * kHkv) top_s[tid >> 3][tid & 7] = 0u;
   __syncthreads();
+  int s0 = 0, s1 = p.num_seqs;
+  if (s1 > G::kThreads) {
+    s1 = first_after<G::kThreads>(0, s1, page_cta, [&](int s) { return p.cu_tokens[s] / BT + 2 * s; });
+    s0 = max(s1 - 1, 0);
+  }
   int mine = -1, my_ctx = 0, my_n = 0;
-  for (int s = tid; s < p.num_seqs; s += G::kThreads) {
+  for (int s = s0 + tid; s < s1; s += G::kThreads) {
     int ctx, n;
     // (a refused chunk is reported by the allocation kernel)
     if (!chunk_fits<BT>(p, s, &ctx, &n) || n == 0) continue;

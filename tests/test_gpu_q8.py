@@ -838,11 +838,22 @@ def test_prefill_as_many_tiles_as_are_sorted(tiles):
 def test_prefill_append_of_many_short_chunks(page):
     """More sequences than the CTA has threads, most of a token or three, some
     empty, some refused (past the table's end, or a negative context)."""
+    _many_short_chunks(page, 1100)
+
+
+def test_prefill_append_of_a_great_many_empty_chunks():
+    """More sequences than the threads squared, 49 in 50 empty."""
+    _many_short_chunks(16, 70000, 0.98)
+
+
+def _many_short_chunks(page, n, empty=0.0):
     rng = np.random.default_rng(page)
-    n = 1100
     lens = rng.integers(0, 4, n)
     lens[[5, 700]] = [2 * page + 1, page]
     ctx = rng.integers(0, 3 * page, n)
+    if empty:
+        gone = rng.random(n) < empty
+        lens[gone] = ctx[gone] = 0
     k, v, q, cu, pool, scales, table, fl, fc = _append_case(40 + page, ctx.tolist(), lens.tolist(), page, layers=1,
                                                             layer=0)
     ctx[[9, 900]] = [-1, table.shape[2] * page]
