@@ -415,8 +415,6 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           const int src = (j % kBatch) * kPagesPerChunk + (lane & (kPagesPerChunk - 1));
           Pages now;
           now.blk = __shfl_sync(0xffffffffu, cur.blk, src);
-          now.sk = __shfl_sync(0xffffffffu, cur.sk, src);
-          now.sv = __shfl_sync(0xffffffffu, cur.sv, src);
           const int pg = j * kPagesPerChunk + (lane & (kPagesPerChunk - 1));
           const bool needed = lane < kPagesPerChunk && pg * BT < it.n_keys;
           const bool valid = needed && now.blk >= 0 && now.blk < p.num_blocks;
@@ -429,6 +427,19 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
           }
           ok = __shfl_sync(0xffffffffu, good, 0) != 0;
           if (!ok) break;
+          // The copies go out before the scales are there (the barrier's bytes are
+          // announced after that: its phase cannot end before).
+          // lane l < 2 kPagesPerChunk: the K rows (l < kPagesPerChunk) or the
+          // V rows of page l mod kPagesPerChunk
+          const int pl = lane & (kPagesPerChunk - 1), kv = (lane / kPagesPerChunk) & 1;
+          // (test hook: CTA 0 leaves this chunk's copies out, so that the
+          // waits on it run out)
+          const bool fault = p.fault_chunk == gc && blockIdx.x == 0;
+          if (!fault && lane < 2 * kPagesPerChunk && ((vm >> pl) & 1u))
+            tma_load_5d(sm.raw[st][kv] + pl * BT * kQ8HeadBytes, &kv_map, 0, it.g, 0, kv, now.blk,
+                        &sm.raw_full[st]);
+          now.sk = __shfl_sync(0xffffffffu, cur.sk, src);
+          now.sv = __shfl_sync(0xffffffffu, cur.sv, src);
           // the chunk's scales are its largest page's (exponent fields)
           const int ek = __float_as_int(now.sk) >> 23, ev = __float_as_int(now.sv) >> 23;
           const int top_k = __reduce_max_sync(0xffffffffu, valid ? ek : 1);
@@ -457,15 +468,6 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             issued_parity = (issued_parity & ~(1u << st)) | (ph << st);
           }
           __syncwarp();
-          // lane l < 2 kPagesPerChunk: the K rows (l < kPagesPerChunk) or the
-          // V rows of page l mod kPagesPerChunk
-          const int pl = lane & (kPagesPerChunk - 1), kv = (lane / kPagesPerChunk) & 1;
-          // (test hook: CTA 0 leaves this chunk's copies out, so that the
-          // waits on it run out)
-          const bool fault = p.fault_chunk == gc && blockIdx.x == 0;
-          if (!fault && lane < 2 * kPagesPerChunk && ((vm >> pl) & 1u))
-            tma_load_5d(sm.raw[st][kv] + pl * BT * kQ8HeadBytes, &kv_map, 0, it.g, 0, kv, now.blk,
-                        &sm.raw_full[st]);
           if (next_has == 1) {
             page_scales(next_g, next);
             next_has = 2;
