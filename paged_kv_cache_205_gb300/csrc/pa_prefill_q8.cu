@@ -24,7 +24,9 @@
 // 2^-25 absolute below 2^-14, which is 2^-32 of the row's largest P.  A chunk
 // whose V scales lie further than 2^7 apart keeps V's bytes as they are and takes
 // log2 sV page by page, so that a heavy key in a page of small scale does not lift
-// the reference by the others' scale.  (K's scales may lie any distance apart: f16
+// the reference by the others' scale; rows whose scores may pass 2^22, where the
+// FMA's unrounded product and the rounded M differ by whole units, take the same
+// way.  (K's scales may lie any distance apart: f16
 // takes a factor down to 2^-15 without rounding, and what is lost below weighs
 // 2^-33 of the largest key's score.)
 // The converter also turns q into f16, a row scaled by a power of two (f undoes
@@ -57,7 +59,8 @@ constexpr int kQThreads = 16 * 32;
 // A score factor's floor: a masked score (-inf) times it stays -inf, and a score
 // of at most 2^28 times it is as good as 0.
 constexpr float kTiny = 1.2e-38f;
-constexpr float kLargeFactor = 0.015625f;   // 2^-6
+constexpr float kLargeFactor = 0.015625f;     // 2^-6
+constexpr uint32_t kOnes = 0x3c003c00u;       // two f16 1.0
 // V scales below 2^-94 (exponent field 33) leave the rest to V's f16 values, so
 // that l = sum P / sV stays in fp32's range (2^15 2^94 for each of 2^18 keys).
 constexpr int kLeastV = 33;
@@ -144,6 +147,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// 8 e4m3 values as f16, and 8 f16 values times m (two f16).
 __device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
   return make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b),
                     e4m3x2_to_f16x2(b >> 16));
@@ -159,16 +163,23 @@ __device__ __forceinline__ uint4 mul8(uint4 a, uint32_t m) {
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
   uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
 }
 
 // The largest |q| (bf16 pattern) of row r of a half's q tile (128-byte rows,
@@ -533,6 +544,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         if (lane == 0) ok = mbar_wait_short(&sm.q_full[qb], (k / kQBufs) & 1, p.wait_ns) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        __syncwarp();   // (what lane 0 waited for, for every lane)
         const int n_chunks = sm.item[qb].n_chunks;
         if (n_chunks == 0) break;
         const int nch = h == 0 ? sm.item[qb].nc0 : sm.item[qb].nc1();
@@ -583,7 +595,7 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
     }
   } else if (warp >= kConvWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQRegsConv));
-      // ================================================== converter warps ==
+    // ================================================== converter warps ==
     // A chunk's bytes as the TMA left them ([128 keys][64] of K and of V) become
     // f16 operand tiles in the swizzled layout that the MMAs read; an item's q
     // becomes f16 first.  V rows past the tile's last key or in a page that was
@@ -634,11 +646,14 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
         const uint4 kr = lds16(src);
         uint4 vr = lds16(src + kChunk * kQ8HeadBytes);
         uint4 w0 = widen8(kr.x, kr.y), w1 = widen8(kr.z, kr.w);
-        if (mul.x != 0x3c003c00u) { w0 = mul8(w0, mul.x); w1 = mul8(w1, mul.x); }
+        if (mul.x != kOnes) {
+          w0 = mul8(w0, mul.x);
+          w1 = mul8(w1, mul.x);
+        }
         sts16(dst, w0);
         sts16(dst + flip, w1);
         if (rec.flags & (kMasked | kDiagonal)) {
-                  if (key >= rec.n_live || !((rec.mask >> (key / BT)) & 1)) vr = make_uint4(0, 0, 0, 0);
+          if (key >= rec.n_live || !((rec.mask >> (key / BT)) & 1)) vr = make_uint4(0, 0, 0, 0);
           // a NaN value would reach the rows before it too (P = 0 times NaN)
           if ((rec.flags & kDiagonal) &&
               (nan_bytes(vr.x) | nan_bytes(vr.y) | nan_bytes(vr.z) | nan_bytes(vr.w)) != 0) {
@@ -650,8 +665,12 @@ __global__ void __launch_bounds__(kQThreads, 1) prefill_attention_q8_kernel(
             sm.nan_item[qb] = items - 1;
           }
         }
-        w0 = widen8(vr.x, vr.y), w1 = widen8(vr.z, vr.w);
-        if (mul.y != 0x3c003c00u) { w0 = mul8(w0, mul.y); w1 = mul8(w1, mul.y); }
+        w0 = widen8(vr.x, vr.y);
+        w1 = widen8(vr.z, vr.w);
+        if (mul.y != kOnes) {
+          w0 = mul8(w0, mul.y);
+          w1 = mul8(w1, mul.y);
+        }
         sts16(dst + to_v, w0);
         sts16(dst + to_v + flip, w1);
         src += 16 * kConvThreads;
